@@ -276,6 +276,8 @@ ZS_API zs_status zs_list_plan_info(zs_list_plan_t plan, int64_t* n_params, int32
 /* Storage format of 16-bit gradients and working copies. */
 #define ZS_FORMAT_BF16 0
 #define ZS_FORMAT_FP16 1
+/* fp32 storage, for the zs_q8_* calls only (the two-pass form keeps to the 16-bit formats). */
+#define ZS_FORMAT_FP32 2
 
 /* Bytes of workspace the two passes need for a shard of n parameters (the
    fp32 gradient, one double per 2048-parameter tile and one per 4096 tiles
@@ -403,6 +405,94 @@ ZS_API void zs_offload_destroy(zs_offload_t ctx);
    copy into param_bf16; all host arrays of n.  Errors: ZS_ERR_NULL, ZS_ERR_RANGE. */
 ZS_API zs_status zs_cpu_adam(const float* gbar, int64_t n, float* master, float* m, float* v, uint16_t* param_bf16,
                              const zs_adam_hp* hp, int64_t step, int32_t threads);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit training operators: activation checkpoints, and a linear layer on them.
+ *
+ * Beside the 16 bytes of state per parameter, a training step holds the layer
+ * inputs that the backward pass reads again (batch size x the layers' input
+ * sizes, kept in 16 bits: "Data Parallelism 数据并行（二）", appendix; chapter
+ * 4.4, §7, activation memory).  zs_q8_save keeps them in 8 bits: one code a
+ * value and one fp32 scale a row (a token).  The same codes are
+ *   - the operand of the layer's 8-bit product, zs_q8_matmul, with a scale for
+ *     each token and each channel of the weight (whose codes zs_q8_save makes
+ *     from the fp32 master or the working copy: a row of a weight is a channel);
+ *   - what zs_q8_weight_grad reads in the backward pass, writing the layer's
+ *     weight gradient as the chunk that zs_reduce_adam_* averages, or adding it
+ *     to earlier micro-batches' sums;
+ *   - what zs_q8_load turns back into values where a layer wants those.
+ *
+ * Matrices are row-major with unit column stride; `ld` is the distance between
+ * rows in elements (at least the columns; not looked at for a single row).
+ * Any alignment of the elements works; code rows that start on 16-byte
+ * boundaries (base and ld), and dy rows that do, run fastest.  Dimensions are
+ * 0 .. 2^31 - 1.  An output may share no byte with an input or another output
+ * (column ranges of one buffer, with one ld, may interleave).  Nothing but the
+ * outputs' own rows and columns is written.  No workspace, no allocation;
+ * every call enqueues kernels on `stream` only and may be captured.  Results
+ * do not depend on what runs beside them, call to call.
+ *
+ * Non-finite values: a row that holds a NaN or an infinity gets the scale NaN
+ * and codes 0, so that everything made from it is NaN and a loss scaler that
+ * looks at the gradients sees it.
+ * ------------------------------------------------------------------------- */
+
+/* Scale rules of zs_q8_save. */
+#define ZS_Q8_SCALE_AMAX 0 /* the row's largest magnitude / 127 */
+#define ZS_Q8_SCALE_POW2 1 /* the least power of two with codes within 127 */
+
+/* Codes of rows.  For row t, with v = x[t][k] * col_scale[k] (one fp32
+   rounding; v = x[t][k] when col_scale is NULL) and a = max_k |v|:
+     ZS_Q8_SCALE_AMAX:  scales[t] = max(f32(a / 127), 2^-126)
+     ZS_Q8_SCALE_POW2:  scales[t] = the least power of two, at least 2^-126,
+                        with a <= 127 * scales[t].  Such codes times their scale
+                        are exact in bf16, so the weight gradient's operands
+                        are exact too; the step is up to twice as wide.
+     codes[t][k] = the exact v / scales[t] rounded to an integer, ties to even.
+   x: rows x cols in x_format (BF16, FP16 or FP32).  col_scale: device fp32
+   array of cols, or NULL: folds a scale that lies along the codes' summed axis
+   into them (the weight's channel scales into dy, for the input gradient).
+   scales: device fp32 array of rows, written.  rows = 0 is a no-op; cols = 0
+   writes the scales of empty rows, 2^-126.
+   Errors: ZS_ERR_NULL, ZS_ERR_RANGE, ZS_ERR_ALIGN, ZS_ERR_ALIAS, ZS_ERR_HIP. */
+ZS_API zs_status zs_q8_save(const void* x, int32_t x_format, int64_t ld_x, int64_t rows, int64_t cols,
+                            const float* col_scale, int32_t scale_rule, int8_t* codes, int64_t ld_codes,
+                            float* scales, zs_stream stream);
+
+/* Values of rows of codes: out[t][k] = codes[t][k] * scales[t] (fp32), rounded
+   to out_format (BF16, FP16 or FP32).  Errors as zs_q8_save. */
+ZS_API zs_status zs_q8_load(const int8_t* codes, int64_t ld_codes, const float* scales, int64_t rows, int64_t cols,
+                            void* out, int32_t out_format, int64_t ld_out, zs_stream stream);
+
+/* The 8-bit matrix product.  w_codes: N x K (a linear layer's weight, N
+   outputs), for both layouts.
+     ZS_Q8_XWT:  x_codes T x K;  y[t][n] = S * x_scales[t] * w_scales[n],
+                 S = sum_k x_codes[t][k] * w_codes[n][k]: the layer's output.
+     ZS_Q8_XW:   x_codes T x N;  y[t][k] = S * x_scales[t] * w_scales[k],
+                 S = sum_n x_codes[t][n] * w_codes[n][k]: the layer's input
+                 gradient, from dy saved with col_scale = the weight's channel
+                 scales, and w_scales = NULL.
+   S is exact (32-bit integers; the summed axis is at most 131,071 long), then
+   f32(S), times each scale in fp32 in that order, rounded to y_format (BF16,
+   FP16 or FP32).  w_scales: device fp32 array of y's columns, or NULL for none.
+   Errors as zs_q8_save. */
+#define ZS_Q8_XWT 0
+#define ZS_Q8_XW 1
+ZS_API zs_status zs_q8_matmul(const int8_t* x_codes, int64_t ld_x, const float* x_scales, const int8_t* w_codes,
+                              int64_t ld_w, const float* w_scales, int64_t T, int64_t N, int64_t K, int32_t layout,
+                              void* y, int32_t y_format, int64_t ld_y, zs_stream stream);
+
+/* The weight gradient of a linear layer from its saved input:
+     dw[n][k] = add[n][k] + sum_t dy[t][n] * (x_codes[t][k] * x_scales[t])
+   dy: T x N in dy_format (BF16 or FP16, taken exactly).  x_codes T x K with
+   scales, as zs_q8_save wrote them; a code times its scale is rounded to bf16
+   (exact for ZS_Q8_SCALE_POW2).  Sums are fp32.  add: NULL for none, or an
+   N x K matrix in dw's format and with dw's ld, which may be dw itself (the
+   sums of earlier micro-batches).  dw: N x K in dw_format (BF16, FP16 or FP32),
+   rounded once.  T = 0 writes add, or zeros.  Errors as zs_q8_save. */
+ZS_API zs_status zs_q8_weight_grad(const void* dy, int32_t dy_format, int64_t ld_dy, const int8_t* x_codes,
+                                   int64_t ld_x, const float* x_scales, int64_t T, int64_t N, int64_t K,
+                                   const void* add, void* dw, int32_t dw_format, int64_t ld_dw, zs_stream stream);
 
 /* Workgroups per launch for all later step calls in this process: 0 picks
    automatically from the device's compute-unit count.  Results do not depend

@@ -149,7 +149,17 @@ _lib.zs_offload_destroy.argtypes = [_vp]
 _lib.zs_cpu_adam.restype = ctypes.c_int
 _lib.zs_cpu_adam.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, ctypes.POINTER(AdamHPStruct), _i64, _i32]
 
+_lib.zs_q8_save.restype = ctypes.c_int
+_lib.zs_q8_save.argtypes = [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp, _i64, _vp, _vp]
+_lib.zs_q8_load.restype = ctypes.c_int
+_lib.zs_q8_load.argtypes = [_vp, _i64, _vp, _i64, _i64, _vp, _i32, _i64, _vp]
+_lib.zs_q8_matmul.restype = ctypes.c_int
+_lib.zs_q8_matmul.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i32, _i64, _vp]
+_lib.zs_q8_weight_grad.restype = ctypes.c_int
+_lib.zs_q8_weight_grad.argtypes = [_vp, _i32, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp]
+
 FORMATS = {"bf16": 0, "fp16": 1}
+Q8_SCALES = {"amax": 0, "pow2": 1}
 
 
 class ZShardError(RuntimeError):
@@ -795,6 +805,126 @@ def reduce_grads_flat_device_scale(grads: Sequence, workspace, sqnorm, scaler: D
                                                       workspace.numel() * workspace.element_size(),
                                                       sqnorm.data_ptr(), _stream_handle(stream, dev)),
                "zs_reduce_grads_flat_device_scale")
+
+
+# ------------------------------------------------------------ 8-bit training operators
+_Q8_FORMATS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_Q8_DY = (torch.bfloat16, torch.float16)
+_Q8_CODES = (torch.int8,)
+
+
+def _matrix(t, dtypes, name):
+    """(address, rows, cols, ld) of a 2-D device tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), rows, cols, ld
+
+
+def _vector(t, n, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected float32")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.numel() != n or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} elements, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _q8_shape(name, got, want):
+    if got != want:
+        raise ValueError(f"{name} is {got[0]} x {got[1]}, expected {want[0]} x {want[1]}")
+
+
+def _q8_call(fn, where, first, others, args, stream):
+    """Calls ``fn`` on the tensors' device (and its current stream by default)."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors live on several devices: {dev}, {t.device}")
+    s = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream_handle(stream, dev)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, s)
+    if st != 0:
+        raise ZShardError(st, where)
+
+
+def q8_save(x, codes, scales, col_scale=None, rule="pow2", stream=None) -> None:
+    """Codes (int8) and scales (fp32, one a row) of the rows of ``x`` (bf16, fp16 or fp32), written to
+    ``codes`` and ``scales``: a layer's input kept for the backward pass, a weight's 8-bit working copy (from
+    its fp32 master or 16-bit copy; a row is a channel), or an output gradient with the weight's channel scales
+    folded in (``col_scale``).  ``rule``: "pow2" (a power of two, exact in the weight gradient) or "amax" (the
+    row's largest magnitude over 127); see zs_q8_save.  Matrices may be views with contiguous rows."""
+    p, rows, cols, ld = _matrix(x, _Q8_FORMATS, "x")
+    q, qr, qc, qld = _matrix(codes, _Q8_CODES, "codes")
+    _q8_shape("codes", (qr, qc), (rows, cols))
+    s = _vector(scales, rows, "scales")
+    c = None if col_scale is None else _vector(col_scale, cols, "col_scale")
+    if rule not in Q8_SCALES:
+        raise ValueError(f"rule must be one of {tuple(Q8_SCALES)}, not {rule!r}")
+    _q8_call(_lib.zs_q8_save, "zs_q8_save", x, (codes, scales, col_scale),
+             (p, _Q8_FORMATS[x.dtype], ld, rows, cols, c, Q8_SCALES[rule], q, qld, s), stream)
+
+
+def q8_load(codes, scales, out, stream=None) -> None:
+    """``out`` (bf16, fp16 or fp32) = ``codes`` times their rows' ``scales``; see zs_q8_load."""
+    q, rows, cols, qld = _matrix(codes, _Q8_CODES, "codes")
+    o, orows, ocols, old = _matrix(out, _Q8_FORMATS, "out")
+    _q8_shape("out", (orows, ocols), (rows, cols))
+    s = _vector(scales, rows, "scales")
+    _q8_call(_lib.zs_q8_load, "zs_q8_load", codes, (scales, out),
+             (q, qld, s, rows, cols, o, _Q8_FORMATS[out.dtype], old), stream)
+
+
+def q8_matmul(x_codes, x_scales, w_codes, w_scales, y, trans_w: bool = True, stream=None) -> None:
+    """The 8-bit product with a scale for each token and channel, into ``y`` (bf16, fp16 or fp32).  ``w_codes``
+    is N x K.  ``trans_w``: x (T x K) times the weight's transpose, a linear layer's output (T x N); otherwise x
+    (T x N) times the weight, its input gradient (T x K).  ``w_scales``: one for each column of ``y``, or None;
+    see zs_q8_matmul."""
+    xp, T, inner, xld = _matrix(x_codes, _Q8_CODES, "x_codes")
+    wp, N, K, wld = _matrix(w_codes, _Q8_CODES, "w_codes")
+    yp, yr, yc, yld = _matrix(y, _Q8_FORMATS, "y")
+    _q8_shape("x_codes", (T, inner), (T, K if trans_w else N))
+    outer = N if trans_w else K
+    _q8_shape("y", (yr, yc), (T, outer))
+    sx = _vector(x_scales, T, "x_scales")
+    sw = None if w_scales is None else _vector(w_scales, outer, "w_scales")
+    _q8_call(_lib.zs_q8_matmul, "zs_q8_matmul", x_codes, (x_scales, w_codes, w_scales, y),
+             (xp, xld, sx, wp, wld, sw, T, N, K, 0 if trans_w else 1, yp, _Q8_FORMATS[y.dtype], yld), stream)
+
+
+def q8_weight_grad(dy, x_codes, x_scales, dw, add=None, stream=None) -> None:
+    """``dw`` (N x K; bf16, fp16 or fp32) = ``add`` + dy^T (x_codes * x_scales): a linear layer's weight gradient
+    from the saved codes of its input (T x K) and its output gradient ``dy`` (T x N; bf16 or fp16).  ``add``: None,
+    or a matrix with ``dw``'s dtype and row stride, ``dw`` itself among them; see zs_q8_weight_grad."""
+    dp, T, N, dld = _matrix(dy, _Q8_DY, "dy")
+    xp, xr, K, xld = _matrix(x_codes, _Q8_CODES, "x_codes")
+    _q8_shape("x_codes", (xr, K), (T, K))
+    wp, wr, wc, wld = _matrix(dw, _Q8_FORMATS, "dw")
+    _q8_shape("dw", (wr, wc), (N, K))
+    s = _vector(x_scales, T, "x_scales")
+    ap = None
+    if add is not None:
+        ap, ar, ac, ald = _matrix(add, (dw.dtype,), "add")
+        _q8_shape("add", (ar, ac), (N, K))
+        if ald != wld and N > 1:
+            raise ValueError(f"add has row stride {ald}, dw {wld}")
+    _q8_call(_lib.zs_q8_weight_grad, "zs_q8_weight_grad", dy, (x_codes, x_scales, dw, add),
+             (dp, _Q8_FORMATS[dy.dtype], dld, xp, xld, s, T, N, K, ap, wp, _Q8_FORMATS[dw.dtype], wld), stream)
 
 
 # ------------------------------------------------------------ optimizer offload

@@ -6,7 +6,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libzshard.so")
 # Device code and HIP-runtime host code compile as HIP in one hipcc command.
-SOURCES = [os.path.join(CSRC, f) for f in ("zs_kernels.hip", "zs_twopass.hip", "zs_api.cpp", "zs_offload.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in ("zs_kernels.hip", "zs_twopass.hip", "zs_q8_rows.hip", "zs_q8_gemm.hip",
+                                           "zs_api.cpp", "zs_offload.cpp", "zs_q8.cpp")]
 # The host AdamW is plain C++ built by the host compiler into an object that
 # the hipcc link takes as is (its AVX2 path is chosen at run time).  Compiling
 # it as a C++ input inside the hipcc command produced a library that crashed

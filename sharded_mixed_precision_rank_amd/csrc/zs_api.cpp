@@ -15,6 +15,7 @@
 
 #include "zs_cpu_adam.h"
 #include "zs_internal.h"
+#include "zs_q8.h"
 #include "zs_twopass.h"
 
 namespace {
@@ -466,6 +467,19 @@ void reduce_shape(const uint16_t* const* g, int32_t N, int64_t n, void* ws, doub
 }  // namespace
 
 namespace zs {
+
+zs_status api_fail(zs_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return fail(st, "%s", buf);
+}
+void api_clear() { g_last_error.clear(); }
+zs_status api_after_launch(hipError_t e, hipStream_t stream, const char* what) {
+  return after_launch(e, stream, what);
+}
 
 zs_status offload_fail(zs_status st, const char* msg) { return fail(st, "%s", msg); }
 

@@ -1,0 +1,563 @@
+"""The 8-bit training operators against plain 64-bit forms on the CPU (tests/q8_ref.py): codes, scales and loaded
+values bit for bit, products and weight gradients within their roundings.  Matrices are views into wider buffers
+filled with a pattern, which has to survive around the outputs."""
+import numpy as np
+import pytest
+import torch
+
+from tests import q8_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DT = ref.DT
+
+
+@pytest.fixture(scope="module")
+def zs():
+    import sharded_mixed_precision_rank_amd as zs
+
+    return zs
+
+
+class Buf:
+    """A rows x cols view with `gap` elements between rows and `lead` before the first, in a buffer of a pattern;
+    one more row and `lead` elements behind."""
+
+    def __init__(self, rows, cols, dtype, gap=0, lead=0, values=None):
+        self.n = lead + (rows + 1) * (cols + gap) + 64
+        pattern = torch.arange(self.n, dtype=torch.int64) % 89 + 1
+        self.flat = pattern.to(dtype).cuda()
+        self.before = self.flat.clone()
+        self.t = self.flat.as_strided((rows, cols), (cols + gap, 1), lead)
+        if values is not None:
+            self.t.copy_(values.to(dtype))
+
+    def untouched_outside(self):
+        a, b = self.flat.clone(), self.before.clone()
+        for x in (a, b):
+            x.as_strided(self.t.shape, self.t.stride(), self.t.storage_offset()).zero_()
+        return torch.equal(a, b)
+
+
+def activations(rng, rows, cols):
+    x = rng.standard_normal((rows, cols)).astype(np.float32)
+    x *= np.exp(rng.standard_normal((rows, 1))).astype(np.float32)
+    x[:, rng.random(cols) < 0.02] *= 20
+    if rows > 2:
+        x[rng.integers(rows)] = 0
+    return torch.from_numpy(x)
+
+
+def random_codes(rng, rows, cols, low=-127):
+    return torch.from_numpy(rng.integers(low, 128, (rows, cols), dtype=np.int8))
+
+
+def random_scales(rng, n, pow2=True):
+    e = rng.integers(-12, 4, n)
+    s = np.ldexp(1.0, e) * (1.0 if pow2 else rng.uniform(1, 2, n))
+    return torch.from_numpy(s.astype(np.float32))
+
+
+def same_bits(a, b):
+    a, b = a.cpu(), b.cpu()
+    nan = torch.isnan(a) if a.is_floating_point() else torch.zeros(a.shape, dtype=torch.bool)
+    if a.is_floating_point():
+        if not torch.equal(nan, torch.isnan(b)):
+            return False
+        a, b = a.masked_fill(nan, 0), b.masked_fill(nan, 0)
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+# ------------------------------------------------------------------ save, load
+SAVE_SHAPES = [(1, 1), (1, 4096), (3, 7), (5, 64), (17, 513), (64, 256), (2, 2049), (3, 8200), (2, 16391), (2, 40001),
+               (1000, 130), (4097, 8)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rule", ["amax", "pow2"])
+@pytest.mark.parametrize("rows,cols", SAVE_SHAPES)
+def test_save_and_load(zs, rows, cols, rule, kind):
+    rng = np.random.default_rng(rows * 7 + cols)
+    for gap_x, gap_q, lead, col in ((0, 0, 0, False), (3, 5, 1, True)):
+        x = activations(rng, rows, cols).to(DT[kind])
+        c = random_scales(rng, cols, pow2=False) if col else None
+        bx = Buf(rows, cols, DT[kind], gap_x, lead, x)
+        bq = Buf(rows, cols, torch.int8, gap_q, lead)
+        bs = Buf(1, rows, torch.float32, 0, lead)
+        zs.q8_save(bx.t, bq.t, bs.t[0], col_scale=None if c is None else c.cuda(), rule=rule)
+        q, s = ref.save(x, rule, c)
+        torch.cuda.synchronize()
+        assert same_bits(bs.t[0], s)
+        assert torch.equal(bq.t.cpu(), q)
+        assert bq.untouched_outside() and bs.untouched_outside()
+        assert same_bits(bx.t, x)
+        for out_kind in DT:
+            bo = Buf(rows, cols, DT[out_kind], gap_x, lead)
+            zs.q8_load(bq.t, bs.t[0], bo.t)
+            torch.cuda.synchronize()
+            assert same_bits(bo.t, ref.load(q, s, out_kind)), out_kind
+            assert bo.untouched_outside()
+
+
+def test_save_rounds_ties_to_even_and_decides_near_borders(zs):
+    """Values at, just above and just below half steps of scales that are no power of two: a product with a rounded
+    reciprocal would put some of them on the wrong side."""
+    rng = np.random.default_rng(3)
+    rows = []
+    for _ in range(200):
+        top = np.float32(np.exp(rng.uniform(-20, 20)))
+        s = np.float64(np.float32(top / np.float32(127)))
+        half = ((rng.integers(-126, 126, 96) + 0.5) * s).astype(np.float32)
+        near = np.concatenate([half, np.nextafter(half, np.float32(np.inf)), np.nextafter(half, np.float32(-np.inf))])
+        rows.append(np.concatenate([[top], np.clip(near, -top, top)]))
+    x = torch.from_numpy(np.stack(rows).astype(np.float32))
+    # exact ties: integer rows whose largest value is 127 have the scale 1
+    tie = torch.arange(-126, 126).float()[None] + 0.5
+    ties = torch.cat([torch.tensor([[127.0]]), tie], 1)
+    for v in (x, ties):
+        for rule in ("amax", "pow2"):
+            q = torch.empty(v.shape, dtype=torch.int8, device="cuda")
+            s = torch.empty(v.shape[0], device="cuda")
+            zs.q8_save(v.cuda(), q, s, rule=rule)
+            wq, ws = ref.save(v, rule)
+            assert same_bits(s, ws) and torch.equal(q.cpu(), wq), rule
+
+
+@pytest.mark.parametrize("rule", ["amax", "pow2"])
+@pytest.mark.parametrize("cols", [5, 300, 5000, 20000])
+def test_save_extremes(zs, rule, cols):
+    """Zero rows, subnormal rows, the largest values, and rows with a NaN or an infinity anywhere."""
+    x = torch.zeros(12, cols)
+    x[1] = 2.0 ** -149
+    x[2] = 127 * 2.0 ** -126
+    x[3, cols - 1] = 3.0e-37
+    x[4] = torch.finfo(torch.float32).max
+    x[5] = 127.0
+    x[6] = 127.00001
+    x[7] = -63.5
+    x[8, 0] = float("nan")
+    x[9, cols - 1] = float("inf")
+    x[10, cols // 2] = -float("inf")
+    x[10, 0] = float("nan")
+    x[11] = -0.0
+    q = torch.full((12, cols), 55, dtype=torch.int8, device="cuda")
+    s = torch.empty(12, device="cuda")
+    zs.q8_save(x.cuda(), q, s, rule=rule)
+    wq, ws = ref.save(x, rule)
+    assert same_bits(s, ws) and torch.equal(q.cpu(), wq)
+    assert torch.isnan(s[8:11]).all() and not q[8:11].any()
+    out = torch.empty(12, cols, dtype=torch.bfloat16, device="cuda")
+    zs.q8_load(q, s, out)
+    assert same_bits(out, ref.load(wq, ws, "bf16"))
+
+
+def test_save_empty_rows(zs):
+    s = torch.zeros(5, device="cuda")
+    zs.q8_save(torch.empty(5, 0, device="cuda"), torch.empty(5, 0, dtype=torch.int8, device="cuda"), s)
+    assert (s.cpu() == 2.0 ** -126).all()
+
+
+def test_saved_values_are_near(zs):
+    """The checkpoint's error: half a step of the row's scale, for every value."""
+    rng = np.random.default_rng(4)
+    x = activations(rng, 300, 1000).to(torch.bfloat16).cuda()
+    q, s = torch.empty(x.shape, dtype=torch.int8, device="cuda"), torch.empty(300, device="cuda")
+    for rule in ("amax", "pow2"):
+        zs.q8_save(x, q, s, rule=rule)
+        off = (q.double() * s.double()[:, None] - x.double()).abs()
+        assert (off <= s.double()[:, None] / 2).all()
+
+
+# ------------------------------------------------------------------ products
+SHAPES = [(1, 1, 1), (1, 64, 64), (1, 300, 200), (2, 17, 1000), (7, 129, 65), (16, 256, 512), (17, 96, 4096), (33, 80, 48),
+          (64, 64, 64), (65, 127, 129), (100, 1, 77), (128, 256, 384), (130, 384, 1111), (257, 513, 272), (300, 700, 640),
+          (513, 300, 144), (1, 5000, 3), (5, 2, 9000)]
+
+
+@pytest.mark.parametrize("trans_w", [True, False])
+@pytest.mark.parametrize("T,N,K", SHAPES)
+def test_matmul(zs, T, N, K, trans_w):
+    rng = np.random.default_rng(T * 31 + N * 7 + K)
+    inner, outer = (K, N) if trans_w else (N, K)
+    # code rows on 16-byte boundaries, then anywhere
+    for case, (pad, lead, gap_y, col) in enumerate(((True, 0, 0, True), (False, 1, 3, False), (True, 16, 8, True))):
+        x, w = random_codes(rng, T, inner), random_codes(rng, N, K)
+        sx, sw = random_scales(rng, T, pow2=False), random_scales(rng, outer, pow2=False) if col else None
+        gap = lambda c: -c % 16 if pad else 5  # noqa: E731
+        bx, bw = Buf(T, inner, torch.int8, gap(inner), lead, x), Buf(N, K, torch.int8, gap(K), lead, w)
+        kind = list(DT)[(case + T) % 3]
+        by = Buf(T, outer, DT[kind], gap_y, lead)
+        zs.q8_matmul(bx.t, sx.cuda(), bw.t, None if sw is None else sw.cuda(), by.t, trans_w=trans_w)
+        torch.cuda.synchronize()
+        y = ref.product(x, sx, w, sw, trans_w)
+        bad = ref.outside(by.t, y, ref.product_tolerance(y, kind), kind)
+        assert not bad.any(), f"{kind} case {case}: {int(bad.sum())} of {bad.numel()} off"
+        assert by.untouched_outside()
+
+
+def test_matmul_sums_are_exact_at_the_longest_axis(zs):
+    """131,071 products of the largest codes: 2,147,467,264, the most that 32 bits must hold; and both signs."""
+    K = 131071
+    x = torch.full((3, K), -128, dtype=torch.int8)
+    x[1] = 127
+    x[2, ::2] = 127
+    w = torch.full((20, K), -128, dtype=torch.int8)
+    w[7] = 127
+    one = torch.ones(3)
+    for trans_w in (True, False):
+        wt = w if trans_w else w.t().contiguous()
+        y = torch.empty(3, 20, device="cuda")
+        zs.q8_matmul(x.cuda(), one.cuda(), wt.cuda(), None, y, trans_w=trans_w)
+        want = (x.double() @ w.double().t()).float()  # f32 of the exact sum
+        assert torch.equal(y.cpu(), want)
+
+
+def test_matmul_nan_scale_marks_its_row_only(zs):
+    rng = np.random.default_rng(5)
+    x, w = random_codes(rng, 40, 96), random_codes(rng, 70, 96)
+    x[3] = 0
+    sx, sw = random_scales(rng, 40), random_scales(rng, 70)
+    sx[3] = float("nan")
+    y = torch.empty(40, 70, dtype=torch.bfloat16, device="cuda")
+    zs.q8_matmul(x.cuda(), sx.cuda(), w.cuda(), sw.cuda(), y)
+    nan = torch.isnan(y.cpu())
+    assert nan[3].all() and int(nan.sum()) == 70
+
+
+# ------------------------------------------------------------------ weight gradient
+@pytest.mark.parametrize("dy_kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,N,K", SHAPES)
+def test_weight_grad(zs, T, N, K, dy_kind):
+    rng = np.random.default_rng(T * 3 + N * 5 + K)
+    for case, (pad, lead, gap_w, add, exact) in enumerate(
+            ((True, 0, 0, False, True), (False, 1, 3, True, True), (True, 16, 8, True, False))):
+        kind = list(DT)[(case + N) % 3]
+        dy = activations(rng, T, N).mul(1e-2).to(DT[dy_kind])
+        x, sx = random_codes(rng, T, K), random_scales(rng, T, pow2=exact)
+        b = activations(rng, N, K).to(DT[kind]) if add else None
+        gap = lambda c, m: -c % m if pad else 5  # noqa: E731
+        bdy = Buf(T, N, DT[dy_kind], gap(N, 8), lead if pad else 1, dy)
+        bx = Buf(T, K, torch.int8, gap(K, 16), lead, x)
+        bw = Buf(N, K, DT[kind], gap_w, lead)
+        ba = Buf(N, K, DT[kind], gap_w, lead, b) if add else None
+        zs.q8_weight_grad(bdy.t, bx.t, sx.cuda(), bw.t, add=ba.t if add else None)
+        torch.cuda.synchronize()
+        want = ref.weight_grad(dy, x, sx, b)
+        bad = ref.outside(bw.t, want, ref.weight_grad_tolerance(dy, x, sx, kind, b, exact), kind)
+        assert not bad.any(), f"{kind} case {case}: {int(bad.sum())} of {bad.numel()} off"
+        assert bw.untouched_outside()
+        if add:  # in place: the same bits
+            zs.q8_weight_grad(bdy.t, bx.t, sx.cuda(), ba.t, add=ba.t)
+            torch.cuda.synchronize()
+            assert same_bits(ba.t, bw.t)
+
+
+def test_weight_grad_without_tokens(zs):
+    dw = torch.ones(5, 9, device="cuda")
+    dy, x, s = (torch.empty(0, 5, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 9, dtype=torch.int8, device="cuda"),
+                torch.empty(0, device="cuda"))
+    add = torch.randn(5, 9, device="cuda")
+    zs.q8_weight_grad(dy, x, s, dw, add=add)
+    assert torch.equal(dw, add)
+    zs.q8_weight_grad(dy, x, s, dw)
+    assert not dw.any()
+
+
+@pytest.mark.parametrize("T,N,K", [(40, 33, 65), (200, 256, 256)])
+def test_weight_grad_non_finite(zs, T, N, K):
+    """A checkpoint row whose scale is NaN makes every weight's gradient NaN; a non-finite dy those of its channel."""
+    rng = np.random.default_rng(6)
+    dy = activations(rng, T, N).to(torch.bfloat16)
+    x, s = random_codes(rng, T, K), random_scales(rng, T)
+    dw = torch.empty(N, K, device="cuda")
+    s2 = s.clone()
+    s2[T // 2] = float("nan")
+    zs.q8_weight_grad(dy.cuda(), x.cuda(), s2.cuda(), dw)
+    assert torch.isnan(dw).all()
+    for kind in ("bf16", "fp16"):
+        d2 = dy.to(DT[kind]).clone()
+        d2[T - 1, 2] = float("inf")
+        x2 = x.clone()
+        x2[T - 1] = 7
+        zs.q8_weight_grad(d2.cuda(), x2.cuda(), s.cuda(), dw)
+        assert torch.isinf(dw[2]).all() and (dw[2] > 0).all()
+        keep = torch.arange(N, device="cuda") != 2
+        assert torch.isfinite(dw[keep]).all()
+
+
+def test_gradients_against_differences(zs):
+    """Input and weight gradients of the layer on codes against central differences of its 64-bit loss
+    L = sum R * (X^ W^T), linear in each argument, so differences are exact up to 64-bit rounding."""
+    rng = np.random.default_rng(7)
+    T, N, K = 9, 20, 33
+    xq, sx = random_codes(rng, T, K), random_scales(rng, T)
+    wq, sw = random_codes(rng, N, K), random_scales(rng, N)
+    R = activations(rng, T, N).to(torch.bfloat16)
+    X, W = xq.double() * sx.double()[:, None], wq.double() * sw.double()[:, None]
+    loss = lambda X, W: float((R.double() * (X @ W.t())).sum())  # noqa: E731
+    dw = torch.empty(N, K, device="cuda")
+    zs.q8_weight_grad(R.cuda(), xq.cuda(), sx.cuda(), dw)
+    g, sg = torch.empty(T, N, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    zs.q8_save(R.cuda(), g, sg, col_scale=sw.cuda(), rule="amax")
+    dx = torch.empty(T, K, device="cuda")
+    zs.q8_matmul(g, sg, wq.cuda(), None, dx, trans_w=False)
+    tol_w = ref.weight_grad_tolerance(R, xq, sx, "fp32")
+    # dx: each of the N codes is off by at most half its scale, times |w code|
+    tol_x = sg.cpu().double()[:, None] / 2 * wq.double().abs().sum(0) * (1 + 2.0 ** -20)
+    for _ in range(40):
+        t, n, k = rng.integers(T), rng.integers(N), rng.integers(K)
+        up, dn = W.clone(), W.clone()
+        up[n, k] += 1
+        dn[n, k] -= 1
+        diff = (loss(X, up) - loss(X, dn)) / 2
+        assert abs(float(dw[n, k]) - diff) <= float(tol_w[n, k]) + 1e-9
+        up, dn = X.clone(), X.clone()
+        up[t, k] += 1
+        dn[t, k] -= 1
+        diff = (loss(up, W) - loss(dn, W)) / 2
+        assert abs(float(dx[t, k]) - diff) <= float(tol_x[t, k]) + 1e-9
+
+
+# ------------------------------------------------------------------ far rows
+def test_rows_beyond_32_bit_offsets(zs):
+    """Rows 2.2 GB apart: element and byte offsets that do not fit 32 bits, in every operand."""
+    far = (1 << 31) + (1 << 27) + 16
+    rng = np.random.default_rng(8)
+    rows, cols = 3, 160
+    big = torch.empty(2 * far + cols + 64, dtype=torch.int8, device="cuda")
+    q = big.as_strided((rows, cols), (far, 1), 0)
+    x = activations(rng, rows, cols)
+    s = torch.empty(rows, device="cuda")
+    zs.q8_save(x.cuda(), q, s)
+    wq, ws = ref.save(x, "pow2")
+    assert torch.equal(q.cpu(), wq) and same_bits(s, ws)
+    out = torch.empty(rows, cols, device="cuda")
+    zs.q8_load(q, s, out)
+    assert same_bits(out, ref.load(wq, ws, "fp32"))
+    w = random_codes(rng, 50, cols)
+    y = torch.empty(rows, 50, device="cuda")
+    one = torch.ones(50, device="cuda")
+    zs.q8_matmul(q, s, w.cuda(), one, y)  # the first operand's rows
+    want = ref.product(wq, ws, w, None, True)
+    assert ((y.cpu().double() - want).abs() <= ref.product_tolerance(want, "fp32")).all()
+    x2, s2 = random_codes(rng, 70, cols), random_scales(rng, 70)
+    y = torch.empty(70, rows, device="cuda")
+    zs.q8_matmul(x2.cuda(), s2.cuda(), q, s, y)  # the weight's rows
+    want = ref.product(x2, s2, wq, ws, True)
+    assert ((y.cpu().double() - want).abs() <= ref.product_tolerance(want, "fp32")).all()
+    x3 = random_codes(rng, 70, rows)
+    y = torch.empty(70, cols, device="cuda")
+    zs.q8_matmul(x3.cuda(), s2.cuda(), q, None, y, trans_w=False)
+    want = ref.product(x3, s2, wq, None, False)
+    assert ((y.cpu().double() - want).abs() <= ref.product_tolerance(want, "fp32")).all()
+    dy = activations(rng, rows, 90).to(torch.bfloat16)
+    dw = torch.empty(90, cols, device="cuda")
+    zs.q8_weight_grad(dy.cuda(), q, s, dw)
+    want = ref.weight_grad(dy, wq, ws)
+    assert ((dw.cpu().double() - want).abs() <= ref.weight_grad_tolerance(dy, wq, ws, "fp32")).all()
+    # 16-bit operands and outputs far apart
+    wide = big.view(torch.bfloat16)
+    far2 = far // 2
+    fdy = wide.as_strided((rows, 90), (far2, 1), 0)
+    fdy.copy_(dy)
+    x4, s4 = random_codes(rng, rows, 40), random_scales(rng, rows)
+    dw = torch.empty(90, 40, device="cuda")
+    zs.q8_weight_grad(fdy, x4.cuda(), s4.cuda(), dw)
+    want = ref.weight_grad(dy, x4, s4)
+    assert ((dw.cpu().double() - want).abs() <= ref.weight_grad_tolerance(dy, x4, s4, "fp32")).all()
+    fy = wide.as_strided((rows, 50), (far2, 1), 0)
+    zs.q8_matmul(wq.cuda(), ws.cuda(), w.cuda(), None, fy)
+    want = ref.product(wq, ws, w, None, True)
+    assert ((fy.cpu().double() - want).abs() <= ref.product_tolerance(want, "bf16")).all()
+    fdw = wide.as_strided((rows, 40), (far2, 1), 0)
+    zs.q8_weight_grad(dy[:, :rows].contiguous().cuda(), x4.cuda(), s4.cuda(), fdw)
+    want = ref.weight_grad(dy[:, :rows], x4, s4)
+    assert ((fdw.cpu().double() - want).abs() <= ref.weight_grad_tolerance(dy[:, :rows], x4, s4, "bf16")).all()
+
+
+# ------------------------------------------------------------------ a training step of a layer
+def test_layer_step_feeds_the_optimizer(zs, orc):
+    """Weight re-cast, forward, checkpoint, backward for two micro-batches on each of two replicas, then the reduce
+    and update: every intermediate against its plain form, the update against the oracle bit for bit."""
+    rng = np.random.default_rng(9)
+    T, N, K = 150, 96, 200
+    dev = torch.device("cuda:0")
+    master = (rng.standard_normal((N, K)) * 0.02).astype(np.float32)
+    P = torch.from_numpy(master.copy()).to(dev)
+    wq, sw = torch.empty(N, K, dtype=torch.int8, device=dev), torch.empty(N, device=dev)
+    zs.q8_save(P, wq, sw, rule="amax")  # the 8-bit working copy, from the fp32 master
+    cq, cs = ref.save(torch.from_numpy(master), "amax")
+    assert torch.equal(wq.cpu(), cq) and same_bits(sw, cs)
+    chunks = []
+    for replica in range(2):
+        sums = torch.zeros(N, K, device=dev)
+        total, slack = torch.zeros(N, K, dtype=torch.float64), torch.zeros(N, K, dtype=torch.float64)
+        for micro in range(2):
+            x = activations(rng, T, K).to(torch.bfloat16)
+            xq, sx = torch.empty(T, K, dtype=torch.int8, device=dev), torch.empty(T, device=dev)
+            zs.q8_save(x.to(dev), xq, sx)
+            rq, rs = ref.save(x, "pow2")
+            assert torch.equal(xq.cpu(), rq) and same_bits(sx, rs)
+            y = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
+            zs.q8_matmul(xq, sx, wq, sw, y)
+            want = ref.product(rq, rs, cq, cs, True)
+            assert ((y.cpu().double() - want).abs() <= ref.product_tolerance(want, "bf16")).all()
+            dy = y.mul(1e-2)
+            gq, sg = torch.empty(T, N, dtype=torch.int8, device=dev), torch.empty(T, device=dev)
+            zs.q8_save(dy, gq, sg, col_scale=sw, rule="amax")
+            dx = torch.empty(T, K, dtype=torch.bfloat16, device=dev)
+            zs.q8_matmul(gq, sg, wq, None, dx, trans_w=False)
+            hq, hs = ref.save(dy.cpu(), "amax", cs)
+            assert torch.equal(gq.cpu(), hq) and same_bits(sg, hs)
+            want = ref.product(hq, hs, cq, None, False)
+            assert ((dx.cpu().double() - want).abs() <= ref.product_tolerance(want, "bf16")).all()
+            out = sums if micro == 0 else torch.empty(N, K, dtype=torch.float32, device=dev)
+            zs.q8_weight_grad(dy, xq, sx, out, add=None if micro == 0 else sums)
+            total += ref.weight_grad(dy.cpu(), rq, rs)
+            slack += ref.weight_grad_tolerance(dy.cpu(), rq, rs, "fp32", sums.cpu() if micro else None)
+            sums = out
+        assert ((sums.cpu().double() - total).abs() <= slack).all()
+        chunks.append(sums.to(torch.bfloat16).reshape(-1).contiguous())
+    n = N * K
+    M, V = torch.zeros(n, device=dev), torch.zeros(n, device=dev)
+    B = torch.zeros(n, dtype=torch.int16, device=dev)
+    hp = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1)
+    zs.reduce_adam_flat(chunks, P.view(-1), M, V, B, hp, 1)
+    G = np.stack([c.view(torch.int16).cpu().numpy().view(np.uint16) for c in chunks])
+    rP, rM, rV, rB = orc.step(G, master.reshape(-1), np.zeros(n, np.float32), np.zeros(n, np.float32), hp, 1)
+    for got, want in ((P.view(-1), rP), (M, rM), (V, rV)):
+        assert np.array_equal(got.cpu().numpy().view(np.uint32), want.view(np.uint32))
+    assert np.array_equal(B.cpu().numpy().view(np.uint16), rB)
+    zs.q8_save(P, wq, sw, rule="amax")  # the next step's working copy
+    cq, cs = ref.save(torch.from_numpy(rP.reshape(N, K)), "amax")
+    assert torch.equal(wq.cpu(), cq) and same_bits(sw, cs)
+
+
+# ------------------------------------------------------------------ streams, graphs
+def _layer(zs, b):
+    zs.q8_save(b["x"], b["xq"], b["sx"])
+    zs.q8_matmul(b["xq"], b["sx"], b["wq"], b["sw"], b["y"])
+    zs.q8_save(b["dy"], b["gq"], b["sg"], col_scale=b["sw"], rule="amax")
+    zs.q8_matmul(b["gq"], b["sg"], b["wq"], None, b["dx"], trans_w=False)
+    zs.q8_weight_grad(b["dy"], b["xq"], b["sx"], b["dw"])
+    zs.q8_weight_grad(b["dy"], b["xq"], b["sx"], b["sums"], add=b["sums"])
+    zs.q8_load(b["xq"], b["sx"], b["back"])
+
+
+def _layer_buffers(rng, T, N, K):
+    dev = "cuda"
+    b = dict(x=activations(rng, T, K).to(torch.bfloat16).cuda(), dy=activations(rng, T, N).to(torch.bfloat16).cuda(),
+             wq=random_codes(rng, N, K).cuda(), sw=random_scales(rng, N).cuda(),
+             xq=torch.empty(T, K, dtype=torch.int8, device=dev), sx=torch.empty(T, device=dev),
+             gq=torch.empty(T, N, dtype=torch.int8, device=dev), sg=torch.empty(T, device=dev),
+             y=torch.empty(T, N, dtype=torch.bfloat16, device=dev), dx=torch.empty(T, K, dtype=torch.bfloat16, device=dev),
+             dw=torch.empty(N, K, dtype=torch.bfloat16, device=dev), sums=torch.zeros(N, K, device=dev),
+             back=torch.empty(T, K, dtype=torch.bfloat16, device=dev))
+    return b
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 256, 512), (70, 130, 250), (512, 512, 768)])
+def test_graph_replays(zs, T, N, K):
+    rng = np.random.default_rng(10)
+    a = _layer_buffers(rng, T, N, K)
+    e = {k: v.clone() for k, v in a.items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _layer(zs, a)
+    torch.cuda.current_stream().wait_stream(side)
+    _layer(zs, e)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _layer(zs, a)
+    for replay in range(4):
+        x, dy = activations(rng, T, K).to(torch.bfloat16).cuda(), activations(rng, T, N).to(torch.bfloat16).cuda()
+        for b in (a, e):
+            b["x"].copy_(x)
+            b["dy"].copy_(dy)
+        graph.replay()
+        _layer(zs, e)
+        torch.cuda.synchronize()
+        for k in a:
+            assert same_bits(a[k], e[k]), (replay, k)
+
+
+def test_two_streams_and_an_explicit_stream(zs):
+    rng = np.random.default_rng(11)
+    bs = [_layer_buffers(rng, 300, 400, 500) for _ in range(2)]
+    want = [{k: v.clone() for k, v in b.items()} for b in bs]
+    for w in want:
+        for _ in range(3):
+            _layer(zs, w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in bs]
+    for _ in range(3):
+        for b, s in zip(bs, streams):
+            with torch.cuda.stream(s):
+                _layer(zs, b)
+    torch.cuda.synchronize()
+    for b, w in zip(bs, want):
+        for k in b:
+            assert same_bits(b[k], w[k]), k
+    s = streams[0]
+    out = torch.empty_like(bs[0]["back"])
+    zs.q8_load(bs[0]["xq"], bs[0]["sx"], out, stream=s)
+    s.synchronize()
+    assert same_bits(out, want[0]["back"])
+
+
+def test_repeated_calls_give_the_same_bits(zs):
+    rng = np.random.default_rng(12)
+    b = _layer_buffers(rng, 700, 384, 640)
+    _layer(zs, b)
+    first = {k: v.clone() for k, v in b.items()}
+    for _ in range(3):
+        b["sums"].zero_()
+        _layer(zs, b)
+        for k in b:
+            assert same_bits(b[k], first[k]), k
+
+
+def test_column_ranges_of_one_buffer(zs):
+    """Outputs that are column ranges of a fused buffer, beside an input that is another range of it."""
+    rng = np.random.default_rng(13)
+    T, K = 37, 64
+    fused = torch.zeros(T, 3 * K, dtype=torch.bfloat16, device="cuda")
+    x = activations(rng, T, K).to(torch.bfloat16)
+    xq, sx = ref.save(x, "pow2")
+    ws = [random_codes(rng, K, K) for _ in range(3)]
+    for i, w in enumerate(ws):
+        zs.q8_matmul(xq.cuda(), sx.cuda(), w.cuda(), None, fused[:, i * K:(i + 1) * K])
+    for i, w in enumerate(ws):
+        want = ref.product(xq, sx, w, None, True)
+        assert ((fused[:, i * K:(i + 1) * K].cpu().double() - want).abs() <= ref.product_tolerance(want, "bf16")).all()
+    zs.q8_load(xq.cuda(), sx.cuda(), fused[:, :K])
+    assert same_bits(fused[:, :K], ref.load(xq, sx, "bf16"))
+    codes = torch.zeros(T, 2 * K, dtype=torch.int8, device="cuda")
+    with pytest.raises(zs.ZShardError):
+        zs.q8_load(codes[:, :K], sx.cuda(), codes.view(torch.bfloat16)[:, :K])
+
+
+def test_refusals_with_device_tensors(zs):
+    q = torch.zeros(8, 16, dtype=torch.int8, device="cuda")
+    s = torch.ones(8, device="cuda")
+    x = torch.zeros(8, 16, device="cuda")
+    with pytest.raises(ValueError, match="expected 8 x 16"):
+        zs.q8_save(x, q[:, :8], s)
+    with pytest.raises(ValueError, match="vector of 8"):
+        zs.q8_save(x, q, s[:4])
+    with pytest.raises(ValueError, match="rule"):
+        zs.q8_save(x, q, s, rule="mean")
+    with pytest.raises(ValueError, match="contiguous rows"):
+        zs.q8_load(q.t(), torch.ones(16, device="cuda"), x.t().contiguous())
+    with pytest.raises(ValueError, match="two dimensions"):
+        zs.q8_load(q[0], s, x)
+    with pytest.raises(zs.ZShardError, match="leading dimension"):
+        zs.q8_save(x[:1].expand(8, 16), q, s)  # rows on top of each other
+    with pytest.raises(ValueError, match="row stride"):
+        zs.q8_weight_grad(x.to(torch.bfloat16), q, s, torch.zeros(16, 16, device="cuda"),
+                          add=torch.zeros(16, 20, device="cuda")[:, :16])
+    with pytest.raises(TypeError, match="dtype"):
+        zs.q8_weight_grad(x.to(torch.bfloat16), q, s, torch.zeros(16, 16, device="cuda"),
+                          add=torch.zeros(16, 16, dtype=torch.bfloat16, device="cuda"))
