@@ -64,16 +64,6 @@ __device__ __forceinline__ void fp16_parts(u32x4 h, u32x4& hi, u32x4& lo) {
   }
 }
 
-// One element's result from its sum, by op.
-template <Q8Op OP>
-struct Out {
-  float rs;  // kNT, kNN: the row's scale
-  __device__ __forceinline__ float of(int32_t acc, const float* cs, int64_t n) const {
-    const float v = (float)acc * rs;
-    return cs ? v * ((const GLB float*)cs)[n] : v;
-  }
-};
-
 // Four results at row m, columns n .. n + 3 (those below N), any format.
 template <int FMT>
 __device__ __forceinline__ void store_row4(const Q8Gemm& a, int64_t m, int64_t n, float* v, bool adds) {
@@ -98,6 +88,36 @@ __device__ __forceinline__ void store4(const Q8Gemm& a, int64_t m, int64_t n, fl
     store_row4<kFP16>(a, m, n, v, adds);
   else
     store_row4<kFP32>(a, m, n, v, adds);
+}
+
+// RUN results at row m from column n on (those below N).
+template <int FMT, int RUN>
+__device__ __forceinline__ void store_run_as(const Q8Gemm& a, int64_t m, int64_t n, const float* v) {
+  const int64_t i = m * a.ldd + n;
+  if (n + RUN <= a.N) {
+    if constexpr (FMT == kFP32 || RUN < 8) {
+#pragma unroll
+      for (int r = 0; r < RUN; r += 4) st_four<FMT>(a.d, i + r, v + r);
+    } else {
+#pragma unroll
+      for (int r = 0; r < RUN; r += 8)
+        st_any<u32x4>((uint16_t*)a.d + i + r, (u32x4){pack_two<FMT>(v[r], v[r + 1]), pack_two<FMT>(v[r + 2], v[r + 3]),
+                                                      pack_two<FMT>(v[r + 4], v[r + 5]), pack_two<FMT>(v[r + 6], v[r + 7])});
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < RUN; ++r)
+      if (n + r < a.N) st_elem<FMT>(a.d, i + r, v[r]);
+  }
+}
+template <int RUN>
+__device__ __forceinline__ void store_run(const Q8Gemm& a, int64_t m, int64_t n, const float* v) {
+  if (a.format == ZS_FORMAT_BF16)
+    store_run_as<kBF16, RUN>(a, m, n, v);
+  else if (a.format == ZS_FORMAT_FP16)
+    store_run_as<kFP16, RUN>(a, m, n, v);
+  else
+    store_run_as<kFP32, RUN>(a, m, n, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -234,14 +254,16 @@ __global__ __launch_bounds__(256) void q8_gemm_any(const Q8Gemm a, int64_t tiles
     for (int i = 0; i < 2; ++i) {
       const int64_t m = m0 + wm + i * 16 + i16;
       if (m >= a.M) continue;
-      Out<OP> out{kT ? 0.0f : ((const GLB float*)a.rs)[m]};
+      const float rs = kT ? 0.0f : ((const GLB float*)a.rs)[m];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int64_t n = n0 + wn + j * 16 + 4 * g;
         float v[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          v[r] = kT ? accf[i][j][r] : n + r < a.N ? out.of(acci[i][j][r], a.cs, n + r) : 0.0f;
+        for (int r = 0; r < 4; ++r) {
+          v[r] = kT ? accf[i][j][r] : (float)acci[i][j][r] * rs;
+          if (!kT && a.cs != nullptr && n + r < a.N) v[r] = v[r] * ((const GLB float*)a.cs)[n + r];
+        }
         if (n < a.N) store4(a, m, n, v, kT && a.add != nullptr);
       }
     }
@@ -258,12 +280,291 @@ hipError_t any_launch(const Q8Gemm& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Code rows on 16-byte boundaries: BM x BN outputs per workgroup of WM x WN
+// waves, pieces of both operands moved from memory into LDS directly, 128
+// codes of K a stage and two stages.  A wave holds its fragments of the next 64
+// codes in registers while the matrix instructions take the current ones, so
+// LDS reads, memory loads and matrix instructions run side by side with one
+// or two waves per SIMD.  One barrier a stage: between its halves every wave has read
+// all of the stage and its part of the next one has arrived.
+// ---------------------------------------------------------------------------
+typedef uint32_t Rsrc __attribute__((ext_vector_type(4)));
+
+// A buffer descriptor over `bytes` bytes at p; loads past them give zeros.
+__device__ __forceinline__ Rsrc make_rsrc(const void* p, int64_t bytes) {
+  const uint64_t b = (uint64_t)p;
+  const uint32_t n = bytes <= 0 ? 0u : bytes > 0x7FFFFFF0ll ? 0x7FFFFFF0u : (uint32_t)(bytes + 3) & ~3u;
+  Rsrc r = {(uint32_t)b, (uint32_t)(b >> 32), n, 0x00020000u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = __builtin_amdgcn_readfirstlane(r[i]);
+  return r;
+}
+
+// 64 lanes' 16 bytes each, from rsrc + voff, to LDS at lds + 16 * lane.  The
+// whole offset is in voff: the bounds check is against that.  The caller waits
+// (vmcnt) before anyone reads them, and before the workgroup ends.
+__device__ __forceinline__ void load_to_lds(Rsrc rsrc, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :
+               : "v"(voff), "s"(rsrc), "s"(lds)
+               : "memory");
+}
+
+// The tile of workgroup `bid`: workgroups go to the eight XCDs in turn, so
+// each XCD takes a run of consecutive tiles, which go down groups of 8 tile
+// rows: its L2 sees few rows and columns of operands at a time.
+__device__ __forceinline__ void tile_of(uint32_t bid, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
+  const uint32_t total = tiles_m * tiles_n;
+  const uint32_t x = bid % 8, per = total / 8, more = total % 8;
+  const uint32_t id = x * per + (x < more ? x : more) + bid / 8;
+  const uint32_t group = id / (8 * tiles_n), first = group * 8;
+  const uint32_t height = tiles_m - first < 8 ? tiles_m - first : 8;
+  const uint32_t in = id % (8 * tiles_n);
+  tm = first + in % height;
+  tn = in / height;
+}
+
+constexpr int kStage = 128;  // codes of K per stage
+
+template <Q8Op OP, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, 1) void q8_gemm_tile(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {
+  constexpr bool kNT = OP == Q8Op::kNT;
+  constexpr int kWaves = WM * WN;
+  constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  constexpr int kABytes = BM * kStage, kBBytes = BN * kStage, kBuf = kABytes + kBBytes;
+  constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = kBBytes / 1024 / kWaves;
+  static_assert(FN % 4 == 0 && kALoads > 0 && kBLoads > 0, "tile shape");
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kBuf];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, i16 = lane & 15;
+  const int wm = wave / WN * TM, wn = wave % WN * TN;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const uint32_t lda = (uint32_t)a.lda, ldb = (uint32_t)a.ldb;
+  const int64_t rows_a = a.M - m0 < BM ? a.M - m0 : BM;
+  const Rsrc ra = make_rsrc((const char*)a.a + m0 * a.lda, (rows_a - 1) * a.lda + a.K);
+  const int32_t K = (int32_t)a.K;
+  const int nk = (K + kStage - 1) / kStage;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS char*)lds;
+
+  // Where a lane's piece of an operand comes from.  Rows of 128 codes are 8
+  // pieces; piece c of row r lies at place c ^ s(r), s = the lane's row in a
+  // fragment & 7, so that the 8 lanes that read one bank width at a time read
+  // 8 different places.
+  const uint32_t va = (uint32_t)(lane >> 3) * lda + (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);
+  uint32_t vb[2];
+  if constexpr (kNT) {
+    // a fragment's row i16 is column (i16 / 4) * 16 + 4 j + i16 % 4 of its 64, which leaves each lane 16
+    // consecutive columns of the result; so s(r) = r % 4 + 4 (r / 16 % 2)
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      vb[p] = (uint32_t)(lane >> 3) * ldb + (uint32_t)(((lane & 7) ^ ((lane >> 3 & 3) | p << 2)) * 16);
+  } else {
+    // rows of K, BN codes each; s(r) = r % 8
+    constexpr int kPer = BN / 16, kRows = 64 / kPer;  // pieces a row, rows a load
+    static_assert(kPer >= 8 && kRows >= 1, "tile width");
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int row = lane / kPer + (p * kRows) % 8;
+      vb[p] = (uint32_t)(lane / kPer) * ldb + (uint32_t)(((lane % kPer) ^ (row & 7)) * 16);
+    }
+  }
+
+  auto load_a = [&](int stage, int j) {
+    const int t = wave * kALoads + j;  // 8 rows each
+    load_to_lds(ra, va + (uint32_t)(t * 8) * lda + (uint32_t)(stage * kStage), lds0 + (stage & 1) * kBuf + t * 1024);
+  };
+  const int64_t rows_n = a.N - n0 < BN ? a.N - n0 : BN;
+  const Rsrc rb_nt = make_rsrc((const char*)a.b + n0 * a.ldb, (rows_n - 1) * a.ldb + a.K);
+  auto load_b = [&](int stage, int j) {
+    const int t = wave * kBLoads + j;
+    const uint32_t to = lds0 + (stage & 1) * kBuf + kABytes + t * 1024;
+    if constexpr (kNT) {
+      load_to_lds(rb_nt, vb[t >> 1 & 1] + (uint32_t)(t * 8) * ldb + (uint32_t)(stage * kStage), to);
+    } else {
+      constexpr int kRows = 64 / (BN / 16);
+      const int64_t k0 = (int64_t)stage * kStage;
+      const int64_t rows = K - k0 < kStage ? K - k0 : kStage;
+      const Rsrc rb = make_rsrc((const char*)a.b + k0 * a.ldb + n0, (rows - 1) * a.ldb + (a.N - n0));
+      load_to_lds(rb, vb[t & 1] + (uint32_t)(t * kRows) * ldb, to);
+    }
+  };
+
+  i32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = (i32x4){0, 0, 0, 0};
+  i32x4 fa[2][FM], fb[2][FN];
+
+  const int s7 = i16 & 7;
+  const int at_a = (wm + i16) * kStage;
+  const int at_b_nt = kABytes + (wn + (i16 >> 2) * 16 + (i16 & 3)) * kStage;
+  const int at_b_nn = kABytes + (16 * g + (i16 >> 1)) * BN + (i16 & 1) * 8;
+  auto read_a = [&](int buf, int half, int i) {
+    fa[half][i] = *(const LDS i32x4*)((LDS char*)lds + buf * kBuf + at_a + i * 16 * kStage + ((4 * half + g) ^ s7) * 16);
+  };
+  auto read_b = [&](int buf, int half, int j) {
+    if constexpr (kNT) {
+      fb[half][j] = *(const LDS i32x4*)((LDS char*)lds + buf * kBuf + at_b_nt + (j / 4 * 64 + j % 4 * 4) * kStage +
+                                        ((4 * half + g) ^ s7) * 16);
+    } else {
+      LDS char* p = (LDS char*)lds + buf * kBuf + at_b_nn + half * 64 * BN + (((wn >> 4) + j) ^ (i16 >> 1)) * 16;
+      const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS i32x2*)p);
+      const i32x2 y = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS i32x2*)(p + 8 * BN));
+      fb[half][j] = (i32x4){x[0], x[1], y[0], y[1]};
+    }
+  };
+  // The last stage's codes past K are whatever the rows go on with: zero them in one operand.  (kNN: rows of b
+  // past K are read as zeros.)
+  auto cut = [&](int stage, int half) {
+    if constexpr (kNT) {
+      if (stage == nk - 1 && K % kStage != 0) {
+        const int left = K - stage * kStage - half * 64 - 16 * g;
+        i32x4 mask;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const int b = left - 4 * d;
+          mask[d] = b >= 4 ? -1 : b <= 0 ? 0 : (1 << (8 * b)) - 1;
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) fa[half][i] &= mask;
+      }
+    }
+  };
+  // The matrix instructions of one half of a stage, with the fragment reads of the next half (of this stage's buffer
+  // or the next one's) and the memory loads of stage `load_stage` spread between them.
+  constexpr int kLoads = kALoads + kBLoads, kMfma = FM * FN;
+  auto half_step = [&](auto half_c, auto read_c, auto load_c, int buf_next, int load_stage) {
+    constexpr int half = decltype(half_c)::value;
+#pragma unroll
+    for (int at = 0; at < kMfma; ++at) {
+      const int i = at / FN, j = at % FN;
+      if constexpr (decltype(read_c)::value) {
+        // the next fragments of a as the present ones come to their last use, those of b in the first half
+        if (j == 0) read_a(buf_next, half ^ 1, i);
+#pragma unroll
+        for (int r = at * 2 * FN / kMfma; r < (at + 1) * 2 * FN / kMfma && r < FN; ++r) read_b(buf_next, half ^ 1, r);
+      }
+      acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[half][j], fa[half][i], acc[i][j], 0, 0, 0);
+      if constexpr (decltype(load_c)::value) {
+#pragma unroll
+        for (int l = at * kLoads / kMfma; l < (at + 1) * kLoads / kMfma; ++l) {
+          if (l < kALoads)
+            load_a(load_stage, l);
+          else
+            load_b(load_stage, l - kALoads);
+        }
+      }
+      if (at % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  typedef std::integral_constant<int, 0> First;
+  typedef std::integral_constant<int, 1> Second;
+  typedef std::true_type Yes;
+  typedef std::false_type No;
+  // Between a stage's halves: this wave has read all of its buffer and its loads of the next have landed; then
+  // every wave's have.
+  auto meet = [&]() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  if (nk > 0) {
+#pragma unroll
+    for (int j = 0; j < kALoads; ++j) load_a(0, j);
+#pragma unroll
+    for (int j = 0; j < kBLoads; ++j) load_b(0, j);
+    meet();
+    if (nk > 1) {
+#pragma unroll
+      for (int j = 0; j < kALoads; ++j) load_a(1, j);
+#pragma unroll
+      for (int j = 0; j < kBLoads; ++j) load_b(1, j);
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) read_b(0, 0, j);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) read_a(0, 0, i);
+    int s = 0;
+    for (; s < nk - 2; ++s) {
+      half_step(First{}, Yes{}, No{}, s & 1, 0);
+      meet();
+      half_step(Second{}, Yes{}, Yes{}, (s + 1) & 1, s + 2);
+    }
+    if (s < nk - 1) {
+      half_step(First{}, Yes{}, No{}, s & 1, 0);
+      meet();
+      half_step(Second{}, Yes{}, No{}, (s + 1) & 1, 0);
+      ++s;
+    }
+    cut(s, 0);
+    half_step(First{}, Yes{}, No{}, s & 1, 0);
+    cut(s, 1);
+    half_step(Second{}, No{}, No{}, 0, 0);
+  }
+
+  // Results: lane i16 holds row i16 of a fragment, kRun consecutive columns from its accumulators.
+  constexpr int kRun = kNT ? 16 : 4;
+  float rs[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = m0 + wm + i * 16 + i16;
+    rs[i] = m < a.M ? ((const GLB float*)a.rs)[m] : 0.0f;
+  }
+#pragma unroll
+  for (int c = 0; c < FN * 4 / kRun; ++c) {
+    const int64_t n = n0 + wn + (kNT ? c * 64 + g * 16 : c * 16 + g * 4);
+    float cs[kRun];
+    if (a.cs != nullptr) {
+#pragma unroll
+      for (int r = 0; r < kRun; ++r) cs[r] = n + r < a.N ? ((const GLB float*)a.cs)[n + r] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int64_t m = m0 + wm + i * 16 + i16;
+      float v[kRun];
+#pragma unroll
+      for (int r = 0; r < kRun; ++r) {
+        v[r] = (float)acc[i][c * kRun / 4 + r / 4][r % 4] * rs[i];
+        if (a.cs != nullptr) v[r] = v[r] * cs[r];
+      }
+      if (m < a.M) store_run<kRun>(a, m, n, v);
+    }
+  }
+}
+
+template <Q8Op OP, int BM, int BN, int WM, int WN>
+hipError_t tile_launch(const Q8Gemm& a, hipStream_t stream) {
+  const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+  q8_gemm_tile<OP, BM, BN, WM, WN><<<dim3((unsigned)(tm * tn)), WM * WN * 64, 0, stream>>>(a, (uint32_t)tm, (uint32_t)tn);
+  return hipGetLastError();
+}
+
+// Code rows that the tiled kernels take: 16-byte rows, offsets within a tile
+// in 31 bits, a grid that a launch can hold.
+bool tiles_fit(const Q8Gemm& a) {
+  const auto rows16 = [](const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 16 == 0 && ld <= (1 << 22); };
+  return rows16(a.a, a.lda) && rows16(a.b, a.ldb) && ((a.M + 127) / 128) * ((a.N + 127) / 128) < (1 << 22);
+}
+
+template <Q8Op OP>
+hipError_t product_launch(const Q8Gemm& a, hipStream_t stream) {
+  if (!tiles_fit(a)) return any_launch<OP, kBF16>(a, stream);
+  const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
+  if (big >= 200) return tile_launch<OP, 256, 256, 2, 4>(a, stream);
+  return tile_launch<OP, 128, 128, 2, 2>(a, stream);
+}
+
 }  // namespace
 
 hipError_t launch_q8_gemm(Q8Op op, const Q8Gemm& a, hipStream_t stream) {
   switch (op) {
-    case Q8Op::kNT: return any_launch<Q8Op::kNT, kBF16>(a, stream);
-    case Q8Op::kNN: return any_launch<Q8Op::kNN, kBF16>(a, stream);
+    case Q8Op::kNT: return product_launch<Q8Op::kNT>(a, stream);
+    case Q8Op::kNN: return product_launch<Q8Op::kNN>(a, stream);
     default:
       return a.a_format == ZS_FORMAT_FP16 ? any_launch<Q8Op::kTN, kFP16>(a, stream)
                                           : any_launch<Q8Op::kTN, kBF16>(a, stream);

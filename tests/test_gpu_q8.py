@@ -195,6 +195,46 @@ def test_matmul(zs, T, N, K, trans_w):
         assert by.untouched_outside()
 
 
+# enough output for the widest tiles, with edges inside them on both sides and at the end of the summed axis
+WIDE = [(4100, 3300, 272), (3333, 4097, 200), (2100, 8200, 1000)]
+
+
+@pytest.mark.parametrize("trans_w", [True, False])
+@pytest.mark.parametrize("rows,cols,inner", WIDE)
+def test_matmul_wide(zs, rows, cols, inner, trans_w):
+    rng = np.random.default_rng(rows)
+    N, K = (cols, inner) if trans_w else (inner, cols)
+    x, w = random_codes(rng, rows, inner), random_codes(rng, N, K)
+    sx, sw = random_scales(rng, rows, pow2=False), random_scales(rng, cols, pow2=False)
+    bx, bw = Buf(rows, inner, torch.int8, -inner % 16, 0, x), Buf(N, K, torch.int8, -K % 16, 16, w)
+    for kind in ("bf16", "fp32"):
+        by = Buf(rows, cols, DT[kind], 3, 1)
+        zs.q8_matmul(bx.t, sx.cuda(), bw.t, sw.cuda(), by.t, trans_w=trans_w)
+        y = ref.product(x.cuda(), sx.cuda(), w.cuda(), sw.cuda(), trans_w).cpu()
+        bad = ref.outside(by.t, y, ref.product_tolerance(y, kind), kind)
+        assert not bad.any(), f"{kind}: {int(bad.sum())} of {bad.numel()} off"
+        assert by.untouched_outside()
+
+
+@pytest.mark.parametrize("dy_kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,cols,inner", WIDE)
+def test_weight_grad_wide(zs, rows, cols, inner, dy_kind):
+    rng = np.random.default_rng(cols)
+    dy = activations(rng, inner, rows).mul(1e-2).to(DT[dy_kind])
+    x, sx = random_codes(rng, inner, cols), random_scales(rng, inner)
+    bdy, bx = Buf(inner, rows, DT[dy_kind], -rows % 8, 0, dy), Buf(inner, cols, torch.int8, -cols % 16, 16, x)
+    dy, x, sx = dy.cuda(), x.cuda(), sx.cuda()
+    for kind in (dy_kind, "fp32"):
+        b = activations(rng, rows, cols).to(DT[kind])
+        bw, ba = Buf(rows, cols, DT[kind], 3, 1), Buf(rows, cols, DT[kind], 3, 1, b)
+        zs.q8_weight_grad(bdy.t, bx.t, sx, bw.t, add=ba.t)
+        want = ref.weight_grad(dy, x, sx, ba.t).cpu()
+        tolerance = ref.weight_grad_tolerance(dy, x, sx, kind, ba.t).cpu()
+        bad = ref.outside(bw.t, want, tolerance, kind)
+        assert not bad.any(), f"{kind}: {int(bad.sum())} of {bad.numel()} off"
+        assert bw.untouched_outside()
+
+
 def test_matmul_sums_are_exact_at_the_longest_axis(zs):
     """131,071 products of the largest codes: 2,147,467,264, the most that 32 bits must hold; and both signs."""
     K = 131071
