@@ -8,6 +8,8 @@
 // operands are bf16: a code times a power of two is exact there, any other
 // scale costs one rounding of half a bf16 step; fp16 gradients are taken as
 // two bf16 parts, which hold them exactly.  Its sums are fp32.
+#include <utility>
+
 #include "zs_q8_dev.h"
 
 namespace zs {
@@ -40,16 +42,15 @@ __device__ __forceinline__ u32x4 ld_piece(const char* row, int64_t col, int64_t 
   return v;
 }
 
-// Codes times their row's scale, as bf16: 16 codes to 32 bytes.
-__device__ __forceinline__ void codes_to_bf16(u32x4 q, float s, u32x4& lo, u32x4& hi) {
-  u32x4 o[2];
+// Eight codes times their row's scale, as bf16.
+__device__ __forceinline__ u32x4 codes_to_bf16(uint32_t q0, uint32_t q1, float s) {
+  u32x4 o;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t w = q[k / 2] >> (16 * (k % 2));
-    o[k / 4][k % 4] = pack_bf16((float)(int8_t)w * s, (float)(int8_t)(w >> 8) * s);
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t w = (k < 2 ? q0 : q1) >> (16 * (k % 2));
+    o[k] = pack_bf16((float)(int8_t)w * s, (float)(int8_t)(w >> 8) * s);
   }
-  lo = o[0];
-  hi = o[1];
+  return o;
 }
 
 // Eight fp16 values as two bf16 parts each: the nearest bf16 and the rest,
@@ -197,10 +198,8 @@ __global__ __launch_bounds__(256) void q8_gemm_any(const Q8Gemm a, int64_t tiles
           *(u32x4*)(lds_a + tid * 16) = ra[0];
         }
         if (tid < 128) {
-          u32x4 lo, hi;
-          codes_to_bf16(rb[0], rscale, lo, hi);
-          *(u32x4*)(lds_b + tid * 32) = lo;
-          *(u32x4*)(lds_b + tid * 32 + 16) = hi;
+          *(u32x4*)(lds_b + tid * 32) = codes_to_bf16(rb[0][0], rb[0][1], rscale);
+          *(u32x4*)(lds_b + tid * 32 + 16) = codes_to_bf16(rb[0][2], rb[0][3], rscale);
         }
       }
       __syncthreads();
@@ -291,14 +290,21 @@ hipError_t any_launch(const Q8Gemm& a, hipStream_t stream) {
 // ---------------------------------------------------------------------------
 typedef uint32_t Rsrc __attribute__((ext_vector_type(4)));
 
-// A buffer descriptor over `bytes` bytes at p; loads past them give zeros.
-__device__ __forceinline__ Rsrc make_rsrc(const void* p, int64_t bytes) {
+// A buffer descriptor over `rows` rows of `width` bytes, `pitch` apart, at p:
+// loads past them give zeros.  The callers keep rows * pitch below 2^31; the
+// last 4 bytes may lie partly past the end, within an aligned word.
+__device__ __forceinline__ Rsrc make_rsrc(const void* p, int32_t rows, int32_t width, int32_t pitch) {
   const uint64_t b = (uint64_t)p;
-  const uint32_t n = bytes <= 0 ? 0u : bytes > 0x7FFFFFF0ll ? 0x7FFFFFF0u : (uint32_t)(bytes + 3) & ~3u;
-  Rsrc r = {(uint32_t)b, (uint32_t)(b >> 32), n, 0x00020000u};
+  const int32_t n = max((rows - 1) * pitch + width + 3, 0) & ~3;  // width <= pitch: 0 without rows
+  Rsrc r = {(uint32_t)b, (uint32_t)(b >> 32), (uint32_t)n, 0x00020000u};
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] = __builtin_amdgcn_readfirstlane(r[i]);
   return r;
+}
+// What is left of `total` after `done`, at most `most`.
+__device__ __forceinline__ int32_t left_of(int64_t total, int64_t done, int32_t most) {
+  const int64_t n = total - done;
+  return n < most ? (int32_t)n : most;
 }
 
 // 64 lanes' 16 bytes each, from rsrc + voff, to LDS at lds + 16 * lane.  The
@@ -327,13 +333,36 @@ __device__ __forceinline__ void tile_of(uint32_t bid, uint32_t tiles_m, uint32_t
 
 constexpr int kStage = 128;  // codes of K per stage
 
+// f of 0 .. N - 1, each a constant: unrolled whatever its size.
+template <class F, int... I>
+__device__ __forceinline__ void for_each(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void for_each(F f) {
+  for_each(f, std::make_integer_sequence<int, N>{});
+}
+typedef std::integral_constant<int, 0> First;
+typedef std::integral_constant<int, 1> Second;
+typedef std::true_type Yes;
+typedef std::false_type No;
+// Between a stage's halves: this wave has read all of its buffer and what it
+// loaded or wrote for the next has landed; then every wave's has.
+__device__ __forceinline__ void meet() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 template <Q8Op OP, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM* WN * 64, 1) void q8_gemm_tile(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {
   constexpr bool kNT = OP == Q8Op::kNT;
   constexpr int kWaves = WM * WN;
   constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
-  constexpr int kABytes = BM * kStage, kBBytes = BN * kStage, kBuf = kABytes + kBBytes;
-  constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = kBBytes / 1024 / kWaves;
+  // kNN: 16 rows of K of b, and 128 bytes that put the next 16 in the other half of the banks
+  constexpr int kGroup = 16 * BN + 128;
+  constexpr int kABytes = BM * kStage, kBBytes = kNT ? BN * kStage : kStage / 16 * kGroup, kBuf = kABytes + kBBytes;
+  constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = BN * kStage / 1024 / kWaves;
   static_assert(FN % 4 == 0 && kALoads > 0 && kBLoads > 0, "tile shape");
   __shared__ __attribute__((aligned(1024))) char lds[2 * kBuf];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -343,9 +372,8 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void q8_gemm_tile(const Q8Gemm a, u
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const uint32_t lda = (uint32_t)a.lda, ldb = (uint32_t)a.ldb;
-  const int64_t rows_a = a.M - m0 < BM ? a.M - m0 : BM;
-  const Rsrc ra = make_rsrc((const char*)a.a + m0 * a.lda, (rows_a - 1) * a.lda + a.K);
   const int32_t K = (int32_t)a.K;
+  const Rsrc ra = make_rsrc((const char*)a.a + m0 * a.lda, left_of(a.M, m0, BM), K, (int32_t)lda);
   const int nk = (K + kStage - 1) / kStage;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS char*)lds;
 
@@ -376,19 +404,18 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void q8_gemm_tile(const Q8Gemm a, u
     const int t = wave * kALoads + j;  // 8 rows each
     load_to_lds(ra, va + (uint32_t)(t * 8) * lda + (uint32_t)(stage * kStage), lds0 + (stage & 1) * kBuf + t * 1024);
   };
-  const int64_t rows_n = a.N - n0 < BN ? a.N - n0 : BN;
-  const Rsrc rb_nt = make_rsrc((const char*)a.b + n0 * a.ldb, (rows_n - 1) * a.ldb + a.K);
+  const int32_t cols = left_of(a.N, n0, BN);
+  const Rsrc rb_nt = make_rsrc((const char*)a.b + n0 * a.ldb, cols, K, (int32_t)ldb);
   auto load_b = [&](int stage, int j) {
     const int t = wave * kBLoads + j;
-    const uint32_t to = lds0 + (stage & 1) * kBuf + kABytes + t * 1024;
+    const uint32_t to = lds0 + (stage & 1) * kBuf + kABytes;
     if constexpr (kNT) {
-      load_to_lds(rb_nt, vb[t >> 1 & 1] + (uint32_t)(t * 8) * ldb + (uint32_t)(stage * kStage), to);
+      load_to_lds(rb_nt, vb[t >> 1 & 1] + (uint32_t)(t * 8) * ldb + (uint32_t)(stage * kStage), to + t * 1024);
     } else {
       constexpr int kRows = 64 / (BN / 16);
-      const int64_t k0 = (int64_t)stage * kStage;
-      const int64_t rows = K - k0 < kStage ? K - k0 : kStage;
-      const Rsrc rb = make_rsrc((const char*)a.b + k0 * a.ldb + n0, (rows - 1) * a.ldb + (a.N - n0));
-      load_to_lds(rb, vb[t & 1] + (uint32_t)(t * kRows) * ldb, to);
+      const int32_t k0 = stage * kStage;
+      const Rsrc rb = make_rsrc((const char*)a.b + k0 * a.ldb + n0, K - k0 < kStage ? K - k0 : kStage, cols, (int32_t)ldb);
+      load_to_lds(rb, vb[t & 1] + (uint32_t)(t * kRows) * ldb, to + t * kRows / 16 * kGroup + t * kRows % 16 * BN);
     }
   };
 
@@ -402,7 +429,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void q8_gemm_tile(const Q8Gemm a, u
   const int s7 = i16 & 7;
   const int at_a = (wm + i16) * kStage;
   const int at_b_nt = kABytes + (wn + (i16 >> 2) * 16 + (i16 & 3)) * kStage;
-  const int at_b_nn = kABytes + (16 * g + (i16 >> 1)) * BN + (i16 & 1) * 8;
+  const int at_b_nn = kABytes + g * kGroup + (i16 >> 1) * BN + (i16 & 1) * 8;
   auto read_a = [&](int buf, int half, int i) {
     fa[half][i] = *(const LDS i32x4*)((LDS char*)lds + buf * kBuf + at_a + i * 16 * kStage + ((4 * half + g) ^ s7) * 16);
   };
@@ -411,7 +438,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void q8_gemm_tile(const Q8Gemm a, u
       fb[half][j] = *(const LDS i32x4*)((LDS char*)lds + buf * kBuf + at_b_nt + (j / 4 * 64 + j % 4 * 4) * kStage +
                                         ((4 * half + g) ^ s7) * 16);
     } else {
-      LDS char* p = (LDS char*)lds + buf * kBuf + at_b_nn + half * 64 * BN + (((wn >> 4) + j) ^ (i16 >> 1)) * 16;
+      LDS char* p = (LDS char*)lds + buf * kBuf + at_b_nn + half * 4 * kGroup + (((wn >> 4) + j) ^ (i16 >> 1)) * 16;
       const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS i32x2*)p);
       const i32x2 y = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS i32x2*)(p + 8 * BN));
       fb[half][j] = (i32x4){x[0], x[1], y[0], y[1]};
@@ -437,40 +464,29 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void q8_gemm_tile(const Q8Gemm a, u
   // The matrix instructions of one half of a stage, with the fragment reads of the next half (of this stage's buffer
   // or the next one's) and the memory loads of stage `load_stage` spread between them.
   constexpr int kLoads = kALoads + kBLoads, kMfma = FM * FN;
+  static_assert(kLoads <= kMfma && 2 * FN <= kMfma, "at most one load beside an instruction");
   auto half_step = [&](auto half_c, auto read_c, auto load_c, int buf_next, int load_stage) {
     constexpr int half = decltype(half_c)::value;
-#pragma unroll
-    for (int at = 0; at < kMfma; ++at) {
-      const int i = at / FN, j = at % FN;
+    for_each<kMfma>([&](auto at_c) {
+      constexpr int at = decltype(at_c)::value, i = at / FN, j = at % FN;
       if constexpr (decltype(read_c)::value) {
         // the next fragments of a as the present ones come to their last use, those of b in the first half
-        if (j == 0) read_a(buf_next, half ^ 1, i);
-#pragma unroll
-        for (int r = at * 2 * FN / kMfma; r < (at + 1) * 2 * FN / kMfma && r < FN; ++r) read_b(buf_next, half ^ 1, r);
+        if constexpr (j == 0) read_a(buf_next, half ^ 1, i);
+        constexpr int lo = at * 2 * FN / kMfma, hi = (at + 1) * 2 * FN / kMfma;
+        if constexpr (hi > lo && lo < FN) read_b(buf_next, half ^ 1, lo);
       }
       acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[half][j], fa[half][i], acc[i][j], 0, 0, 0);
       if constexpr (decltype(load_c)::value) {
-#pragma unroll
-        for (int l = at * kLoads / kMfma; l < (at + 1) * kLoads / kMfma; ++l) {
-          if (l < kALoads)
+        constexpr int l = at * kLoads / kMfma;
+        if constexpr ((at + 1) * kLoads / kMfma > l) {
+          if constexpr (l < kALoads)
             load_a(load_stage, l);
           else
             load_b(load_stage, l - kALoads);
         }
       }
-      if (at % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  typedef std::integral_constant<int, 0> First;
-  typedef std::integral_constant<int, 1> Second;
-  typedef std::true_type Yes;
-  typedef std::false_type No;
-  // Between a stage's halves: this wave has read all of its buffer and its loads of the next have landed; then
-  // every wave's have.
-  auto meet = [&]() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+      if constexpr (at % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    });
   };
 
   if (nk > 0) {
@@ -559,15 +575,282 @@ hipError_t product_launch(const Q8Gemm& a, hipStream_t stream) {
   return tile_launch<OP, 128, 128, 2, 2>(a, stream);
 }
 
+// ---------------------------------------------------------------------------
+// The weight gradient in tiles of BM x BN by WM x WN waves, 64 rows of tokens
+// a stage and two stages, by the schedule of q8_gemm_tile.  Both operands lie
+// as they do in memory, a token's values side by side, and are turned by the
+// transposing LDS reads.  The codes go through registers, where they become
+// bf16 once for the whole workgroup (in the fragments each wave would convert
+// them again).  dy goes to LDS directly (kDirect), or through registers: as two
+// bf16 parts of 32 tokens a stage when it is fp16 (kParts, kPartsAny), or as it
+// is (kThrough).  kDirect and kParts want rows on 16-byte boundaries, the others
+// take any.
+// ---------------------------------------------------------------------------
+enum class DyPath { kDirect, kParts, kThrough, kPartsAny };
+
+// Sixteen bytes of a buffer (zeros past its end).
+__device__ __forceinline__ u32x4 ld_buffer16(Rsrc r, uint32_t voff) {
+  const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)((uint64_t)r[0] | (uint64_t)r[1] << 32), 0, (int)r[2], 0x00020000);
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)voff, 0, 0));
+}
+__device__ __forceinline__ float ld_buffer4(Rsrc r, uint32_t voff) {
+  const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)((uint64_t)r[0] | (uint64_t)r[1] << 32), 0, (int)r[2], 0x00020000);
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, (int)voff, 0, 0));
+}
+
+template <DyPath PATH, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM* WN * 64, 1) void q8_grad_tile(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {
+  constexpr int kThreads = WM * WN * 64, kWaves = WM * WN;
+  constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  constexpr bool kTwo = PATH == DyPath::kParts || PATH == DyPath::kPartsAny;
+  constexpr bool kAligned = PATH == DyPath::kDirect || PATH == DyPath::kParts;
+  constexpr int kRows = kTwo ? 32 : 64;  // tokens a stage
+  // 8 rows, and 128 bytes that put the next 8 in the other half of the banks
+  constexpr int kGroup = 8 * BM * 2 + 128;
+  constexpr int kABytes = 8 * kGroup, kBuf = 2 * kABytes;
+  constexpr int kPer = BM / 8;                                   // pieces of 16 bytes in a row of dy
+  constexpr int kALoads = 64 * BM * 2 / 1024 / kWaves;           // direct loads of a wave a stage
+  constexpr int kAPieces = kRows * kPer / kThreads;              // pieces of dy of a thread a stage
+  constexpr int kXPieces = kRows * (BN / 16) / kThreads;         // pieces of codes of a thread a stage
+  constexpr int kARows = kThreads / kPer, kXRows = kThreads / (BN / 16);  // rows from a thread's piece to its next
+  static_assert(kALoads > 0 && kAPieces > 0 && kXPieces > 0 && kPer >= 16 && kARows % 8 == 0 && kXRows % 8 == 0,
+                "tile shape");
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kBuf];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, i16 = lane & 15;
+  const int wm = wave / WN * TM, wn = wave % WN * TN;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int32_t T = (int32_t)a.K;
+  const int nk = (int)(((int64_t)T + kRows - 1) / kRows);
+  // tokens left at a stage (the difference is right even where stage * kRows passes 2^31)
+  auto rows_at = [&](int stage) {
+    const int32_t n = (int32_t)((uint32_t)T - (uint32_t)stage * (uint32_t)kRows);
+    return n < kRows ? n : kRows;
+  };
+  const int32_t wide_a = left_of(a.M, m0, BM) * 2, wide_b = left_of(a.N, n0, BN);
+  const int32_t pitch_a = (int32_t)a.lda * 2, pitch_b = (int32_t)a.ldb;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS char*)lds;
+
+  // Piece c of row r lies at place c ^ s(r).  A transposing read takes 32
+  // bytes of 4 consecutive rows, and of 4 that lie 8 rows on, per 32 lanes: s puts those 4 at different places.
+  auto s_of = [](int row) { return (row & 3) << 1; };
+  auto at_row = [](int row) { return row / 8 * kGroup + row % 8 * BM * 2; };
+
+  auto rsrc_a = [&](int stage) {
+    return make_rsrc((const char*)a.a + ((int64_t)stage * kRows * a.lda + m0) * 2, rows_at(stage), wide_a, pitch_a);
+  };
+  // dy, directly: a load is 64 / kPer rows; loads 4 rows apart share s
+  constexpr int kApart = 4 / (64 / kPer);
+  uint32_t va[kApart];
+  if constexpr (PATH == DyPath::kDirect) {
+#pragma unroll
+    for (int j = 0; j < kApart; ++j) {
+      const int row = (wave * kALoads + j) * (64 / kPer) + lane / kPer;
+      va[j] = (uint32_t)row * (uint32_t)pitch_a + (uint32_t)(((lane % kPer) ^ s_of(row)) * 16);
+    }
+  }
+  auto direct_a = [&](int stage, int j) {
+    load_to_lds(rsrc_a(stage), va[j % kApart] + (uint32_t)(j / kApart * 4) * (uint32_t)pitch_a,
+                lds0 + (stage & 1) * kBuf + at_row((wave * kALoads + j) * (64 / kPer)));
+  };
+  // dy, through registers: a thread's pieces lie kARows rows apart, at places that many groups apart
+  u32x4 ar[PATH == DyPath::kDirect ? 1 : kAPieces];
+  const int row_a = tid / kPer, row_x = tid / (BN / 16);
+  auto fetch_a = [&](int stage, int c) {
+    if constexpr (kAligned) {
+      ar[c] = ld_buffer16(rsrc_a(stage), (uint32_t)(row_a * pitch_a + tid % kPer * 16) + (uint32_t)(c * kARows * pitch_a));
+    } else {
+      const int64_t t = (int64_t)stage * kRows + row_a + c * kARows;
+      ar[c] = ld_piece<2>((const char*)a.a + t * a.lda * 2, m0 * 2 + tid % kPer * 16, a.M * 2, t < T);
+    }
+  };
+  auto put_a = [&](int stage, int c) {
+    LDS char* to = (LDS char*)lds + ((stage & 1) * kBuf + at_row(row_a) + ((tid % kPer) ^ s_of(row_a)) * 16) +
+                   c * kARows / 8 * kGroup;
+    if constexpr (kTwo) {
+      u32x4 hi, lo;
+      fp16_parts(ar[c], hi, lo);
+      *(LDS u32x4*)to = hi;
+      *(LDS u32x4*)(to + 4 * kGroup) = lo;  // 32 rows on: the same s
+    } else {
+      *(LDS u32x4*)to = ar[c];
+    }
+  };
+  // codes, the same way
+  u32x4 xr[kXPieces];
+  float xs[kXPieces];
+  auto fetch_x = [&](int stage, int c) {
+    if constexpr (kAligned) {
+      const int64_t t0 = (int64_t)stage * kRows;
+      const int32_t rows = rows_at(stage);
+      xr[c] = ld_buffer16(make_rsrc((const char*)a.b + t0 * a.ldb + n0, rows, wide_b, pitch_b),
+                          (uint32_t)(row_x * pitch_b + tid % (BN / 16) * 16) + (uint32_t)(c * kXRows * pitch_b));
+      xs[c] = ld_buffer4(make_rsrc(a.rs + t0, rows, 4, 4), (uint32_t)(row_x * 4) + c * kXRows * 4);
+    } else {
+      const int64_t t = (int64_t)stage * kRows + row_x + c * kXRows;
+      xr[c] = ld_piece<1>((const char*)a.b + t * a.ldb, n0 + tid % (BN / 16) * 16, a.N, t < T);
+      xs[c] = t < T ? ((const GLB float*)a.rs)[t] : 0.0f;
+    }
+  };
+  auto put_x = [&](int stage, int c, int part) {  // part: 8 of a piece's 16 codes
+    LDS char* to = (LDS char*)lds +
+                   ((stage & 1) * kBuf + kABytes + at_row(row_x) + ((tid % (BN / 16) * 2) ^ s_of(row_x)) * 16) +
+                   c * kXRows / 8 * kGroup;
+    *(LDS u32x4*)(to + part * 16) = codes_to_bf16(xr[c][2 * part], xr[c][2 * part + 1], xs[c]);
+  };
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
+  bf16x8 fa[2][FM], fb[2][FN];
+  // A lane's place in the rows of a read, for each of the four values that s leaves of a fragment's first piece.
+  // A and b have rows of one width, so these serve both.
+  static_assert(BM == BN && TM % 64 == 0 && TN % 64 == 0, "one set of places");
+  uint32_t place[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    place[v] = (uint32_t)(g * kGroup + (i16 >> 2) * BM * 2 + ((2 * v + (i16 >> 1 & 1)) ^ (i16 >> 2) << 1) * 16 + (i16 & 1) * 8);
+  auto turned = [&](uint32_t at, int col16) {  // 8 tokens (4 and 4) of the 16 columns from 16 * col16
+    LDS char* p = (LDS char*)lds + (place[col16 & 3] + at) + (col16 >> 2) * 128;
+    const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)p);
+    const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(p + 4 * BM * 2));
+    return __builtin_bit_cast(bf16x8, (i16x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+  };
+  auto read_a = [&](int buf, int half, int i) {
+    fa[half][i] = turned((uint32_t)(buf * kBuf + half * 4 * kGroup + wm * 2), i);
+  };
+  auto read_b = [&](int buf, int half, int j) {  // both parts of dy meet the same codes
+    fb[half][j] = turned((uint32_t)(buf * kBuf + kABytes + (kTwo ? 0 : half * 4) * kGroup + wn * 2), j);
+  };
+
+  constexpr int kMfma = FM * FN;
+  constexpr int kMoves = (PATH == DyPath::kDirect ? kALoads : kAPieces) + 2 * kXPieces;
+  static_assert(kMoves <= kMfma && 2 * FN <= kMfma, "at most one move beside an instruction");
+  auto half_step = [&](auto half_c, auto read_c, auto load_c, int buf_next, int stage) {
+    constexpr int half = decltype(half_c)::value;
+    for_each<kMfma>([&](auto at_c) {
+      constexpr int at = decltype(at_c)::value, i = at / FN, j = at % FN;
+      if constexpr (decltype(read_c)::value) {
+        if constexpr (j == 0) read_a(buf_next, half ^ 1, i);
+        // b's fragments in the second half of the instructions
+        constexpr int lo = at * 2 * FN / kMfma - FN, hi = (at + 1) * 2 * FN / kMfma - FN;
+        if constexpr (lo >= 0 && hi > lo) read_b(buf_next, half ^ 1, lo);
+      }
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[half][j], fa[half][i], acc[i][j], 0, 0, 0);
+      if constexpr (decltype(load_c)::value) {
+        // what was fetched for `stage` goes to LDS and its place is fetched again for the stage after it
+        constexpr int l = at * kMoves / kMfma;
+        if constexpr ((at + 1) * kMoves / kMfma > l) {
+          if constexpr (l < 2 * kXPieces) {
+            put_x(stage, l / 2, l % 2);
+            if constexpr (l % 2) fetch_x(stage + 1, l / 2);
+          } else if constexpr (PATH == DyPath::kDirect) {
+            direct_a(stage, l - 2 * kXPieces);
+          } else {
+            put_a(stage, l - 2 * kXPieces);
+            fetch_a(stage + 1, l - 2 * kXPieces);
+          }
+        }
+      }
+      if constexpr (at % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  auto fetch = [&](int stage) {
+#pragma unroll
+    for (int c = 0; c < kXPieces; ++c) fetch_x(stage, c);
+    if constexpr (PATH != DyPath::kDirect) {
+#pragma unroll
+      for (int c = 0; c < kAPieces; ++c) fetch_a(stage, c);
+    }
+  };
+  auto put = [&](int stage) {
+#pragma unroll
+    for (int c = 0; c < 2 * kXPieces; ++c) put_x(stage, c / 2, c % 2);
+    if constexpr (PATH == DyPath::kDirect) {
+#pragma unroll
+      for (int j = 0; j < kALoads; ++j) direct_a(stage, j);
+    } else {
+#pragma unroll
+      for (int c = 0; c < kAPieces; ++c) put_a(stage, c);
+    }
+  };
+  if (nk > 0) {
+    fetch(0);
+    put(0);
+    fetch(1);
+    meet();
+    if (nk > 1) put(1);
+    fetch(2);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) read_b(0, 0, j);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) read_a(0, 0, i);
+    int k = 0;
+    for (; k < nk - 2; ++k) {
+      half_step(First{}, Yes{}, No{}, k & 1, 0);
+      meet();
+      half_step(Second{}, Yes{}, Yes{}, (k + 1) & 1, k + 2);
+    }
+    if (k < nk - 1) {
+      half_step(First{}, Yes{}, No{}, k & 1, 0);
+      meet();
+      half_step(Second{}, Yes{}, No{}, (k + 1) & 1, 0);
+      ++k;
+    }
+    half_step(First{}, Yes{}, No{}, k & 1, 0);
+    half_step(Second{}, No{}, No{}, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = m0 + wm + i * 16 + i16;
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int64_t n = n0 + wn + j * 16 + g * 4;
+      float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      if (n < a.N) store4(a, m, n, v, a.add != nullptr);
+    }
+  }
+}
+
+template <DyPath PATH, int BM, int BN, int WM, int WN>
+hipError_t grad_tile_launch(const Q8Gemm& a, hipStream_t stream) {
+  const uint32_t tm = (uint32_t)((a.M + BM - 1) / BM), tn = (uint32_t)((a.N + BN - 1) / BN);
+  q8_grad_tile<PATH, BM, BN, WM, WN><<<dim3(tm * tn), WM * WN * 64, 0, stream>>>(a, tm, tn);
+  return hipGetLastError();
+}
+
+hipError_t grad_launch(const Q8Gemm& a, hipStream_t stream) {
+  const bool two = a.a_format == ZS_FORMAT_FP16;
+  const int64_t small = ((a.M + 127) / 128) * ((a.N + 127) / 128);
+  const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
+  if (small < 64 || small >= (1 << 22))
+    return two ? any_launch<Q8Op::kTN, kFP16>(a, stream) : any_launch<Q8Op::kTN, kBF16>(a, stream);
+  const bool aligned = (uintptr_t)a.a % 16 == 0 && a.lda % 8 == 0 && a.lda <= (1 << 22) && (uintptr_t)a.b % 16 == 0 &&
+                       a.ldb % 16 == 0 && a.ldb <= (1 << 22);
+  if (!aligned)
+    return two ? grad_tile_launch<DyPath::kPartsAny, 128, 128, 2, 2>(a, stream)
+               : grad_tile_launch<DyPath::kThrough, 128, 128, 2, 2>(a, stream);
+  if (big >= 200)
+    return two ? grad_tile_launch<DyPath::kParts, 256, 256, 2, 4>(a, stream)
+               : grad_tile_launch<DyPath::kDirect, 256, 256, 2, 4>(a, stream);
+  return two ? grad_tile_launch<DyPath::kParts, 128, 128, 2, 2>(a, stream)
+             : grad_tile_launch<DyPath::kDirect, 128, 128, 2, 2>(a, stream);
+}
+
 }  // namespace
 
 hipError_t launch_q8_gemm(Q8Op op, const Q8Gemm& a, hipStream_t stream) {
   switch (op) {
     case Q8Op::kNT: return product_launch<Q8Op::kNT>(a, stream);
     case Q8Op::kNN: return product_launch<Q8Op::kNN>(a, stream);
-    default:
-      return a.a_format == ZS_FORMAT_FP16 ? any_launch<Q8Op::kTN, kFP16>(a, stream)
-                                          : any_launch<Q8Op::kTN, kBF16>(a, stream);
+    default: return grad_launch(a, stream);
   }
 }
 
