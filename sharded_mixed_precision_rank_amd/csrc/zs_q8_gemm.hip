@@ -317,6 +317,18 @@ __device__ __forceinline__ void load_to_lds(Rsrc rsrc, uint32_t voff, uint32_t l
                : "memory");
 }
 
+// Sixteen bytes of a buffer (zeros past its end).
+__device__ __forceinline__ u32x4 ld_buffer16(Rsrc r, uint32_t voff) {
+  const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)((uint64_t)r[0] | (uint64_t)r[1] << 32), 0, (int)r[2], 0x00020000);
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)voff, 0, 0));
+}
+__device__ __forceinline__ float ld_buffer4(Rsrc r, uint32_t voff) {
+  const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)((uint64_t)r[0] | (uint64_t)r[1] << 32), 0, (int)r[2], 0x00020000);
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, (int)voff, 0, 0));
+}
+
 // The tile of workgroup `bid`: workgroups go to the eight XCDs in turn, so
 // each XCD takes a run of consecutive tiles, which go down groups of 8 tile
 // rows: its L2 sees few rows and columns of operands at a time.
@@ -346,25 +358,34 @@ typedef std::integral_constant<int, 0> First;
 typedef std::integral_constant<int, 1> Second;
 typedef std::true_type Yes;
 typedef std::false_type No;
-// Between a stage's halves: this wave has read all of its buffer and what it
-// loaded or wrote for the next has landed; then every wave's has.
+// Between a stage's halves: this wave has read all of its buffer, and all but
+// its last LATER loads have landed (and what it wrote); then every wave's have.
+template <int LATER>
 __device__ __forceinline__ void meet() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  static_assert(LATER >= 0 && LATER < 64, "a 6-bit count");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(LATER) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
-template <Q8Op OP, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM* WN * 64, 1) void q8_gemm_tile(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {
+// The xor of a piece's place in row r of b's rows of K.
+template <int BN>
+__device__ __forceinline__ int place_nn(int r) {
+  return BN > 64 ? r & 7 : (r >> 2 & 1) | (r >> 4 & 1) << 1;
+}
+
+template <Q8Op OP, int BM, int BN, int WM, int WN, int NS>
+__global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {
   constexpr bool kNT = OP == Q8Op::kNT;
   constexpr int kWaves = WM * WN;
   constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
-  // kNN: 16 rows of K of b, and 128 bytes that put the next 16 in the other half of the banks
-  constexpr int kGroup = 16 * BN + 128;
+  // kNN: 16 rows of K of b, and 128 bytes that put the next 16 in the other half of the banks (rows of 4 pieces do
+  // that by their places)
+  constexpr int kGroup = 16 * BN + (BN > 64 ? 128 : 0);
   constexpr int kABytes = BM * kStage, kBBytes = kNT ? BN * kStage : kStage / 16 * kGroup, kBuf = kABytes + kBBytes;
   constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = BN * kStage / 1024 / kWaves;
-  static_assert(FN % 4 == 0 && kALoads > 0 && kBLoads > 0, "tile shape");
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kBuf];
+  static_assert(FN % 4 == 0 && kALoads > 0 && kBLoads > 0 && (NS & (NS - 1)) == 0, "tile shape");
+  __shared__ __attribute__((aligned(1024))) char lds[NS * kBuf];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, i16 = lane & 15;
   const int wm = wave / WN * TM, wn = wave % WN * TN;
@@ -390,31 +411,33 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void q8_gemm_tile(const Q8Gemm a, u
     for (int p = 0; p < 2; ++p)
       vb[p] = (uint32_t)(lane >> 3) * ldb + (uint32_t)(((lane & 7) ^ ((lane >> 3 & 3) | p << 2)) * 16);
   } else {
-    // rows of K, BN codes each; s(r) = r % 8
+    // rows of K, BN codes each; s(r) = r % 8, or with 4 pieces a row r / 4 % 2 + 2 (r / 16 % 2)
     constexpr int kPer = BN / 16, kRows = 64 / kPer;  // pieces a row, rows a load
-    static_assert(kPer >= 8 && kRows >= 1, "tile width");
+    static_assert(kPer >= 4 && kRows >= 1, "tile width");
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      const int row = lane / kPer + (p * kRows) % 8;
-      vb[p] = (uint32_t)(lane / kPer) * ldb + (uint32_t)(((lane % kPer) ^ (row & 7)) * 16);
+      const int row = lane / kPer + p * kRows;
+      vb[p] = (uint32_t)(lane / kPer) * ldb + (uint32_t)(((lane % kPer) ^ place_nn<BN>(row)) * 16);
     }
   }
 
+  // A stage past the last lies past the end of every buffer: zeros, and no traffic (offsets in a tile are below 2^31).
+  auto from = [&](int stage) { return stage < nk ? (uint32_t)(stage * kStage) : 0x7FFFFFF0u; };
   auto load_a = [&](int stage, int j) {
     const int t = wave * kALoads + j;  // 8 rows each
-    load_to_lds(ra, va + (uint32_t)(t * 8) * lda + (uint32_t)(stage * kStage), lds0 + (stage & 1) * kBuf + t * 1024);
+    load_to_lds(ra, va + (uint32_t)(t * 8) * lda + from(stage), lds0 + (stage & (NS - 1)) * kBuf + t * 1024);
   };
   const int32_t cols = left_of(a.N, n0, BN);
   const Rsrc rb_nt = make_rsrc((const char*)a.b + n0 * a.ldb, cols, K, (int32_t)ldb);
   auto load_b = [&](int stage, int j) {
     const int t = wave * kBLoads + j;
-    const uint32_t to = lds0 + (stage & 1) * kBuf + kABytes;
+    const uint32_t to = lds0 + (stage & (NS - 1)) * kBuf + kABytes;
     if constexpr (kNT) {
-      load_to_lds(rb_nt, vb[t >> 1 & 1] + (uint32_t)(t * 8) * ldb + (uint32_t)(stage * kStage), to + t * 1024);
+      load_to_lds(rb_nt, vb[t >> 1 & 1] + (uint32_t)(t * 8) * ldb + from(stage), to + t * 1024);
     } else {
       constexpr int kRows = 64 / (BN / 16);
       const int32_t k0 = stage * kStage;
-      const Rsrc rb = make_rsrc((const char*)a.b + k0 * a.ldb + n0, K - k0 < kStage ? K - k0 : kStage, cols, (int32_t)ldb);
+      const Rsrc rb = make_rsrc((const char*)a.b + k0 * a.ldb + n0, max(min(K - k0, kStage), 0), cols, (int32_t)ldb);
       load_to_lds(rb, vb[t & 1] + (uint32_t)(t * kRows) * ldb, to + t * kRows / 16 * kGroup + t * kRows % 16 * BN);
     }
   };
@@ -438,7 +461,9 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void q8_gemm_tile(const Q8Gemm a, u
       fb[half][j] = *(const LDS i32x4*)((LDS char*)lds + buf * kBuf + at_b_nt + (j / 4 * 64 + j % 4 * 4) * kStage +
                                         ((4 * half + g) ^ s7) * 16);
     } else {
-      LDS char* p = (LDS char*)lds + buf * kBuf + at_b_nn + half * 4 * kGroup + (((wn >> 4) + j) ^ (i16 >> 1)) * 16;
+      // rows r and r + 8 share s
+      LDS char* p = (LDS char*)lds + buf * kBuf + at_b_nn + half * 4 * kGroup +
+                    (((wn >> 4) + j) ^ place_nn<BN>(16 * g + (i16 >> 1))) * 16;
       const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS i32x2*)p);
       const i32x2 y = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS i32x2*)(p + 8 * BN));
       fb[half][j] = (i32x4){x[0], x[1], y[0], y[1]};
@@ -448,7 +473,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void q8_gemm_tile(const Q8Gemm a, u
   // past K are read as zeros.)
   auto cut = [&](int stage, int half) {
     if constexpr (kNT) {
-      if (stage == nk - 1 && K % kStage != 0) {
+      if (K % kStage != 0) {
         const int left = K - stage * kStage - half * 64 - 16 * g;
         i32x4 mask;
 #pragma unroll
@@ -461,66 +486,54 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void q8_gemm_tile(const Q8Gemm a, u
       }
     }
   };
-  // The matrix instructions of one half of a stage, with the fragment reads of the next half (of this stage's buffer
-  // or the next one's) and the memory loads of stage `load_stage` spread between them.
+  // The matrix instructions of one half of a stage, with the fragment reads of the next half and, in the second, the
+  // memory loads of stage `stage` + NS (into the buffer of the present one) spread between them.
   constexpr int kLoads = kALoads + kBLoads, kMfma = FM * FN;
-  static_assert(kLoads <= kMfma && 2 * FN <= kMfma, "at most one load beside an instruction");
-  auto half_step = [&](auto half_c, auto read_c, auto load_c, int buf_next, int load_stage) {
+  auto half_step = [&](auto half_c, int stage) {
     constexpr int half = decltype(half_c)::value;
+    const int buf_next = (stage + half) & (NS - 1);
+    if (stage == nk - 1) cut(stage, half);
     for_each<kMfma>([&](auto at_c) {
       constexpr int at = decltype(at_c)::value, i = at / FN, j = at % FN;
-      if constexpr (decltype(read_c)::value) {
-        // the next fragments of a as the present ones come to their last use, those of b in the first half
-        if constexpr (j == 0) read_a(buf_next, half ^ 1, i);
-        constexpr int lo = at * 2 * FN / kMfma, hi = (at + 1) * 2 * FN / kMfma;
-        if constexpr (hi > lo && lo < FN) read_b(buf_next, half ^ 1, lo);
-      }
+      // the next fragments of a as the present ones come to their last use, those of b in the first half
+      if constexpr (j == 0) read_a(buf_next, half ^ 1, i);
+      for_each<FN>([&](auto r) {
+        if constexpr (r >= at * 2 * FN / kMfma && r < (at + 1) * 2 * FN / kMfma) read_b(buf_next, half ^ 1, r);
+      });
       acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[half][j], fa[half][i], acc[i][j], 0, 0, 0);
-      if constexpr (decltype(load_c)::value) {
-        constexpr int l = at * kLoads / kMfma;
-        if constexpr ((at + 1) * kLoads / kMfma > l) {
-          if constexpr (l < kALoads)
-            load_a(load_stage, l);
-          else
-            load_b(load_stage, l - kALoads);
-        }
+      if constexpr (half == 1) {
+        for_each<kLoads>([&](auto l) {
+          if constexpr (l >= at * kLoads / kMfma && l < (at + 1) * kLoads / kMfma) {
+            if constexpr (l < kALoads)
+              load_a(stage + NS, l);
+            else
+              load_b(stage + NS, l - kALoads);
+          }
+        });
       }
       if constexpr (at % 4 == 3) __builtin_amdgcn_sched_barrier(0);
     });
   };
-
+  // The ring: stage s lies in buffer s % NS; stage s + NS is loaded into it once every wave has read the last of s.
   if (nk > 0) {
 #pragma unroll
-    for (int j = 0; j < kALoads; ++j) load_a(0, j);
+    for (int p = 0; p < NS; ++p) {
 #pragma unroll
-    for (int j = 0; j < kBLoads; ++j) load_b(0, j);
-    meet();
-    if (nk > 1) {
+      for (int j = 0; j < kALoads; ++j) load_a(p, j);
 #pragma unroll
-      for (int j = 0; j < kALoads; ++j) load_a(1, j);
-#pragma unroll
-      for (int j = 0; j < kBLoads; ++j) load_b(1, j);
+      for (int j = 0; j < kBLoads; ++j) load_b(p, j);
     }
+    meet<(NS - 1) * kLoads>();
 #pragma unroll
     for (int j = 0; j < FN; ++j) read_b(0, 0, j);
 #pragma unroll
     for (int i = 0; i < FM; ++i) read_a(0, 0, i);
-    int s = 0;
-    for (; s < nk - 2; ++s) {
-      half_step(First{}, Yes{}, No{}, s & 1, 0);
-      meet();
-      half_step(Second{}, Yes{}, Yes{}, (s + 1) & 1, s + 2);
+    for (int s = 0; s < nk; ++s) {
+      half_step(First{}, s);
+      meet<(NS - 2) * kLoads>();  // all but the stages after the next have landed
+      half_step(Second{}, s);
     }
-    if (s < nk - 1) {
-      half_step(First{}, Yes{}, No{}, s & 1, 0);
-      meet();
-      half_step(Second{}, Yes{}, No{}, (s + 1) & 1, 0);
-      ++s;
-    }
-    cut(s, 0);
-    half_step(First{}, Yes{}, No{}, s & 1, 0);
-    cut(s, 1);
-    half_step(Second{}, No{}, No{}, 0, 0);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way to LDS when the workgroup ends
   }
 
   // Results: lane i16 holds row i16 of a fragment, kRun consecutive columns from its accumulators.
@@ -553,26 +566,225 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void q8_gemm_tile(const Q8Gemm a, u
   }
 }
 
-template <Q8Op OP, int BM, int BN, int WM, int WN>
-hipError_t tile_launch(const Q8Gemm& a, hipStream_t stream) {
-  const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
-  q8_gemm_tile<OP, BM, BN, WM, WN><<<dim3((unsigned)(tm * tn)), WM * WN * 64, 0, stream>>>(a, (uint32_t)tm, (uint32_t)tn);
+// ---------------------------------------------------------------------------
+// Few rows of x: 16 MT x 16 NT outputs per workgroup, whose W waves each take
+// every W-th 64 codes of the summed axis, so that the weight's bytes are
+// spread over many waves although the outputs are few.  No wave needs
+// another's operands: kNT reads fragments from memory straight into
+// registers; kNN moves them through a part of LDS of the wave's own, to turn
+// the weight's rows.  The waves' sums meet in LDS (integer additions, whose
+// order does not matter).
+// ---------------------------------------------------------------------------
+template <Q8Op OP, int MT, int NT, int W>
+__global__ __launch_bounds__(W * 64, 2) void q8_gemm_split(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {
+  constexpr bool kNT = OP == Q8Op::kNT;
+  constexpr int BM = MT * 16, BN = NT * 16;
+  constexpr int kPitch = BN + 4;                       // of the sums in LDS: lanes of an instruction in 64 banks
+  constexpr int kSums = BM * kPitch * 4;
+  constexpr int kStageBytes = kNT ? 0 : (MT + NT) * 1024;  // a wave's operands of one step
+  constexpr int kLds = 2 * W * kStageBytes > kSums ? 2 * W * kStageBytes : kSums;
+  __shared__ __attribute__((aligned(1024))) char lds[kLds];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, i16 = lane & 15;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int32_t K = (int32_t)a.K, steps = (K + 63) / 64;
+  const int32_t lda = (int32_t)a.lda, ldb = (int32_t)a.ldb, cols = left_of(a.N, n0, BN);
+  const Rsrc ra = make_rsrc((const char*)a.a + m0 * a.lda, left_of(a.M, m0, BM), K, lda);
+
+  i32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = (i32x4){0, 0, 0, 0};
+  // codes of a past K, in the step that holds its end
+  auto cut = [&](int step, i32x4* fa) {
+    if (step * 64 + 64 > K) {
+      const int left = K - step * 64 - 16 * g;
+      i32x4 mask;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const int b = left - 4 * d;
+        mask[d] = b >= 4 ? -1 : b <= 0 ? 0 : (1 << (8 * b)) - 1;
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fa[i] &= mask;
+    }
+  };
+  if constexpr (kNT) {
+    const Rsrc rb = make_rsrc((const char*)a.b + n0 * a.ldb, cols, K, ldb);
+    const uint32_t va = (uint32_t)(i16 * lda + g * 16), vb = (uint32_t)(i16 * ldb + g * 16);
+    constexpr int kAhead = MT * NT >= 16 ? 2 : 4;  // steps in flight
+    i32x4 fa[kAhead][MT], fb[kAhead][NT];
+    auto fetch = [&](int step, int u) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fb[u][j] = __builtin_bit_cast(i32x4, ld_buffer16(rb, vb + j * 16 * ldb + step * 64));
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fa[u][i] = __builtin_bit_cast(i32x4, ld_buffer16(ra, va + i * 16 * lda + step * 64));
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) fetch(wave + u * W, u);
+    for (int step = wave; step < steps; step += kAhead * W) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int at = step + u * W;
+        if (at < steps) {
+          cut(at, fa[u]);
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[u][j], fa[u][i], acc[i][j], 0, 0, 0);
+        }
+        fetch(at + kAhead * W, u);
+      }
+    }
+  } else {
+    // a step's rows of a: 64 codes, 4 pieces, piece c of row r at place c ^ (r / 2 % 4); its 64 rows of b: NT
+    // pieces, at place c ^ s(r) where there are four
+    const uint32_t mine = (uint32_t)(uintptr_t)(LDS char*)lds + wave * 2 * kStageBytes;
+    auto s_of = [](int r) { return NT == 4 ? (r >> 2 & 1) | (r >> 4 & 1) << 1 : 0; };
+    const uint32_t va = (uint32_t)((lane >> 2) * lda + ((lane & 3) ^ (lane >> 3 & 3)) * 16);
+    auto fetch = [&](int step, int buf) {
+      const int32_t k0 = step * 64;
+      const Rsrc rb = make_rsrc((const char*)a.b + (int64_t)k0 * a.ldb + n0, K - k0 < 64 ? K - k0 : 64, cols, ldb);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) load_to_lds(ra, va + i * 16 * lda + k0, mine + buf * kStageBytes + i * 1024);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int row = j * (64 / NT) + lane / NT;
+        load_to_lds(rb, (uint32_t)(row * ldb + ((lane % NT) ^ s_of(row)) * 16),
+                    mine + buf * kStageBytes + MT * 1024 + j * 1024);
+      }
+    };
+    int buf = 0;
+    if (wave < steps) fetch(wave, 0);
+    for (int step = wave; step < steps; step += W, buf ^= 1) {
+      // what was read from the other buffer has been used
+      if (step + W < steps) {
+        fetch(step + W, buf ^ 1);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(MT + NT) : "memory");
+      } else {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      }
+      LDS char* p = (LDS char*)lds + wave * 2 * kStageBytes + buf * kStageBytes;
+      i32x4 fa[MT], fb[NT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fa[i] = *(LDS i32x4*)(p + i * 1024 + i16 * 64 + (g ^ (i16 >> 1 & 3)) * 16);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int row = 16 * g + (i16 >> 1);
+        LDS char* q = p + MT * 1024 + row * BN + (i16 & 1) * 8;
+        const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS i32x2*)(q + (j ^ s_of(row)) * 16));
+        const i32x2 y = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS i32x2*)(q + 8 * BN + (j ^ s_of(row + 8)) * 16));
+        fb[j] = (i32x4){x[0], x[1], y[0], y[1]};
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+    __syncthreads();  // the operands' LDS is done with
+  }
+  int32_t* sums = (int32_t*)lds;
+  for (int i = tid; i < BM * kPitch; i += W * 64) sums[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        __hip_atomic_fetch_add(&sums[(i * 16 + i16) * kPitch + (j * 4 + r) * 4 + g], acc[i][j][r], __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_WORKGROUP);
+  __syncthreads();
+  for (int i = tid; i < BM * (BN / 4); i += W * 64) {
+    const int row = i / (BN / 4), four = i % (BN / 4);  // columns 4 * four .. + 3: j = four / 4, g = four % 4
+    const int64_t m = m0 + row, n = n0 + four * 4;
+    if (m >= a.M || n >= a.N) continue;
+    const float rs = ((const GLB float*)a.rs)[m];
+    float v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      v[r] = (float)sums[row * kPitch + (four / 4 * 4 + r) * 4 + four % 4] * rs;
+      if (a.cs != nullptr && n + r < a.N) v[r] = v[r] * ((const GLB float*)a.cs)[n + r];
+    }
+    store4(a, m, n, v, false);
+  }
+}
+
+template <Q8Op OP, int MT, int NT, int W>
+hipError_t split_launch(const Q8Gemm& a, hipStream_t stream) {
+  const uint32_t tm = (uint32_t)((a.M + MT * 16 - 1) / (MT * 16)), tn = (uint32_t)((a.N + NT * 16 - 1) / (NT * 16));
+  q8_gemm_split<OP, MT, NT, W><<<dim3(tm * tn), W * 64, 0, stream>>>(a, tm, tn);
   return hipGetLastError();
 }
 
-// Code rows that the tiled kernels take: 16-byte rows, offsets within a tile
-// in 31 bits, a grid that a launch can hold.
-bool tiles_fit(const Q8Gemm& a) {
-  const auto rows16 = [](const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 16 == 0 && ld <= (1 << 22); };
-  return rows16(a.a, a.lda) && rows16(a.b, a.ldb) && ((a.M + 127) / 128) * ((a.N + 127) / 128) < (1 << 22);
+template <Q8Op OP, int BM, int BN, int WM, int WN, int NS>
+hipError_t tile_launch(const Q8Gemm& a, hipStream_t stream) {
+  const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+  q8_gemm_tile<OP, BM, BN, WM, WN, NS><<<dim3((unsigned)(tm * tn)), WM * WN * 64, 0, stream>>>(a, (uint32_t)tm, (uint32_t)tn);
+  return hipGetLastError();
+}
+
+// Code rows that the tiled kernels take: 16-byte rows (a single row at any
+// distance from the next), offsets within a tile below 2^31, a grid that a
+// launch can hold.
+bool rows16(const void* p, int64_t rows, int64_t ld) {
+  return (uintptr_t)p % 16 == 0 && (rows <= 1 || (ld % 16 == 0 && ld <= (1 << 22)));
+}
+int64_t tiles_of(const Q8Gemm& a, int64_t bm, int64_t bn) { return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn); }
+constexpr int64_t kMostTiles = 1 << 22;
+
+// The tile of a product with 16-byte rows, by the time of one stage of 128
+// codes that its grid needs in all, measured on 256 compute units at K = 4096
+// and 11008 (us):
+//   256 x 256, one workgroup a unit: 1.15-1.45 for a first round of up to 256
+//     tiles, 1.7-1.9 a round where there are more;
+//   128 x 128: 0.45-0.7 up to 256 tiles with four stages, beyond that two
+//     workgroups of two stages a unit, 0.8-1.15 for each 512;
+//   64 x 64: 0.25-0.33 up to 256 tiles, 0.45-0.5 for each 512.
+// For example 8192 x 11008 by 4096: 346 / 407 / 616 us; 2000 x 4096: 44.7 /
+// 36.2 / 59.5; 1000 x 4096: 42.4 / 21.8 / 31.2; 333 x 4096: 41.5 / 16.5 /
+// 15.2; 61 x 11008: 38.6 / 16.2 / 10.7.
+enum class Tile { k64, k128, k128Far, k256 };
+Tile tile_for(const Q8Gemm& a) {
+  const auto rounds = [](int64_t t, int64_t at_once) { return (double)((t + at_once - 1) / at_once); };
+  const int64_t t64 = tiles_of(a, 64, 64), t128 = tiles_of(a, 128, 128), t256 = tiles_of(a, 256, 256);
+  const double c64 = t64 <= 256 ? 0.30 : 0.475 * rounds(t64, 512);
+  const double c128 = t128 <= 256 ? 0.50 + 0.18 * (double)t128 / 256 : t128 <= 512 ? 0.65 + 0.45 * (double)t128 / 512 : 1.1 * rounds(t128, 512);
+  const double c256 = t256 <= 256 ? 1.40 : 1.8 * rounds(t256, 256);
+  if (c64 <= c128 && c64 <= c256) return Tile::k64;
+  if (c128 <= c256) return t128 <= 256 ? Tile::k128Far : Tile::k128;
+  return Tile::k256;
 }
 
 template <Q8Op OP>
-hipError_t product_launch(const Q8Gemm& a, hipStream_t stream) {
-  if (!tiles_fit(a)) return any_launch<OP, kBF16>(a, stream);
-  const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-  if (big >= 200) return tile_launch<OP, 256, 256, 2, 4>(a, stream);
-  return tile_launch<OP, 128, 128, 2, 2>(a, stream);
+hipError_t product_launch(const Q8Gemm& given, hipStream_t stream) {
+  Q8Gemm a = given;
+  const int64_t rows_b = OP == Q8Op::kNT ? a.N : a.K;
+  if (!rows16(a.a, a.M, a.lda) || !rows16(a.b, rows_b, a.ldb) || tiles_of(a, 64, 64) >= kMostTiles)
+    return any_launch<OP, kBF16>(a, stream);
+  // a single row: any distance that holds what a tile reads of it
+  if (a.M <= 1) a.lda = (a.K + 15) / 16 * 16;
+  if (rows_b <= 1) a.ldb = OP == Q8Op::kNT ? (a.K + 15) / 16 * 16 : 256;
+  // Few rows: their tiles of 64 columns may be too few to draw on all of the memory.  One token, K = 4096: 6.2 us
+  // against 9.2 in 64 x 64 tiles for N = 4096, 11.8 against 10.0 for N = 11008; 16 tokens 7.8 / 9.4 and 16.3 / 9.8.
+  // kNN: 10.6 / 11.5 with N = K = 4096, 10.7 / 11.9 with N = 4096 rows of K = 11008.
+  if constexpr (OP == Q8Op::kNT) {
+    if (a.M <= 16 && (a.N + 63) / 64 <= 96) return split_launch<OP, 1, 1, 4>(a, stream);
+  } else {
+    if (a.M <= 16) return split_launch<OP, 1, 4, 8>(a, stream);
+  }
+  switch (tile_for(a)) {
+    case Tile::k64: return tile_launch<OP, 64, 64, 4, 1, 4>(a, stream);
+    case Tile::k128Far: return tile_launch<OP, 128, 128, 4, 2, 4>(a, stream);
+    case Tile::k128: return tile_launch<OP, 128, 128, 2, 2, 2>(a, stream);
+    default: return tile_launch<OP, 256, 256, 2, 4, 2>(a, stream);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -588,20 +800,8 @@ hipError_t product_launch(const Q8Gemm& a, hipStream_t stream) {
 // ---------------------------------------------------------------------------
 enum class DyPath { kDirect, kParts, kThrough, kPartsAny };
 
-// Sixteen bytes of a buffer (zeros past its end).
-__device__ __forceinline__ u32x4 ld_buffer16(Rsrc r, uint32_t voff) {
-  const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)((uint64_t)r[0] | (uint64_t)r[1] << 32), 0, (int)r[2], 0x00020000);
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)voff, 0, 0));
-}
-__device__ __forceinline__ float ld_buffer4(Rsrc r, uint32_t voff) {
-  const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)((uint64_t)r[0] | (uint64_t)r[1] << 32), 0, (int)r[2], 0x00020000);
-  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, (int)voff, 0, 0));
-}
-
 template <DyPath PATH, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM* WN * 64, 1) void q8_grad_tile(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {
+__global__ __launch_bounds__(WM* WN * 64, 2) void q8_grad_tile(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {
   constexpr int kThreads = WM * WN * 64, kWaves = WM * WN;
   constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr bool kTwo = PATH == DyPath::kParts || PATH == DyPath::kPartsAny;
@@ -784,7 +984,7 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void q8_grad_tile(const Q8Gemm a, u
     fetch(0);
     put(0);
     fetch(1);
-    meet();
+    meet<0>();
     if (nk > 1) put(1);
     fetch(2);
 #pragma unroll
@@ -794,12 +994,12 @@ __global__ __launch_bounds__(WM* WN * 64, 1) void q8_grad_tile(const Q8Gemm a, u
     int k = 0;
     for (; k < nk - 2; ++k) {
       half_step(First{}, Yes{}, No{}, k & 1, 0);
-      meet();
+      meet<0>();
       half_step(Second{}, Yes{}, Yes{}, (k + 1) & 1, k + 2);
     }
     if (k < nk - 1) {
       half_step(First{}, Yes{}, No{}, k & 1, 0);
-      meet();
+      meet<0>();
       half_step(Second{}, Yes{}, No{}, (k + 1) & 1, 0);
       ++k;
     }
@@ -826,14 +1026,14 @@ hipError_t grad_tile_launch(const Q8Gemm& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t grad_launch(const Q8Gemm& a, hipStream_t stream) {
+hipError_t grad_launch(const Q8Gemm& given, hipStream_t stream) {
+  Q8Gemm a = given;
   const bool two = a.a_format == ZS_FORMAT_FP16;
-  const int64_t small = ((a.M + 127) / 128) * ((a.N + 127) / 128);
-  const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-  if (small < 64 || small >= (1 << 22))
+  const int64_t small = tiles_of(a, 128, 128), big = tiles_of(a, 256, 256);
+  if (small < 64 || small >= kMostTiles)
     return two ? any_launch<Q8Op::kTN, kFP16>(a, stream) : any_launch<Q8Op::kTN, kBF16>(a, stream);
-  const bool aligned = (uintptr_t)a.a % 16 == 0 && a.lda % 8 == 0 && a.lda <= (1 << 22) && (uintptr_t)a.b % 16 == 0 &&
-                       a.ldb % 16 == 0 && a.ldb <= (1 << 22);
+  const bool aligned = rows16(a.a, a.K, a.lda * 2) && rows16(a.b, a.K, a.ldb);
+  if (aligned && a.K <= 1) a.lda = a.ldb = 256;  // a single row: any distance that holds what a tile reads of it
   if (!aligned)
     return two ? grad_tile_launch<DyPath::kPartsAny, 128, 128, 2, 2>(a, stream)
                : grad_tile_launch<DyPath::kThrough, 128, 128, 2, 2>(a, stream);
