@@ -809,57 +809,63 @@ def reduce_grads_flat_device_scale(grads: Sequence, workspace, sqnorm, scaler: D
 
 # ------------------------------------------------------------ 8-bit training operators
 _Q8_FORMATS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_Q8_DY = (torch.bfloat16, torch.float16)
-_Q8_CODES = (torch.int8,)
+_Q8_DY = {torch.bfloat16: 0, torch.float16: 1}
+_Q8_CODES = {torch.int8: -1}
+# The current stream's raw handle by device index, without building a torch.cuda.Stream (1.9 us, of a call's 8)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _matrix(t, dtypes, name):
-    """(address, rows, cols, ld) of a 2-D device tensor whose rows are contiguous."""
+def _q8_refuse(t, formats, name):
+    """Raises for what :func:`_matrix` or :func:`_vector` could not take apart."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
-    rows, cols = t.shape
-    ld, step = t.stride()
+    if t.dtype not in formats:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(formats)}")
+    raise ValueError(f"{name} must have two dimensions, not {t.dim()}")
+
+
+def _matrix(t, formats, name):
+    """(address, rows, columns, row stride, format) of a 2-D tensor whose rows are contiguous."""
+    try:
+        fmt = formats[t.dtype]
+        rows, cols = t.shape
+        ld, step = t.stride()
+        p = t.data_ptr()
+    except (KeyError, AttributeError, ValueError):
+        _q8_refuse(t, formats, name)
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), rows, cols, ld
+    return p, rows, cols, ld, fmt
 
 
 def _vector(t, n, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not torch.float32:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected float32")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.numel() != n or t.dim() != 1 or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
+        _q8_refuse(t, (torch.float32,), name)
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous vector of {n} elements, not {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _q8_shape(name, got, want):
-    if got != want:
-        raise ValueError(f"{name} is {got[0]} x {got[1]}, expected {want[0]} x {want[1]}")
+def _q8_shape(name, rows, cols, want_rows, want_cols):
+    raise ValueError(f"{name} is {rows} x {cols}, expected {want_rows} x {want_cols}")
 
 
-def _q8_call(fn, where, first, others, args, stream):
+def _q8_call(fn, where, tensors, args, stream):
     """Calls ``fn`` on the tensors' device (and its current stream by default)."""
-    dev = first.device
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors live on several devices: {dev}, {t.device}")
-    s = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream_handle(stream, dev)
-    if torch.cuda.current_device() == dev.index:
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != index or not t.is_cuda:
+            if not all(x.is_cuda for x in tensors):
+                raise ValueError(f"{where}: every array must be a device tensor")
+            raise ValueError(f"tensors live on several devices: {tensors[0].device}, {t.device}")
+    s = _raw_stream(index) if stream is None else _stream_handle(stream, tensors[0].device)
+    if torch.cuda.current_device() == index:
         st = fn(*args, s)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             st = fn(*args, s)
-    if st != 0:
+    if st:
         raise ZShardError(st, where)
 
 
@@ -869,25 +875,27 @@ def q8_save(x, codes, scales, col_scale=None, rule="pow2", stream=None) -> None:
     its fp32 master or 16-bit copy; a row is a channel), or an output gradient with the weight's channel scales
     folded in (``col_scale``).  ``rule``: "pow2" (a power of two, exact in the weight gradient) or "amax" (the
     row's largest magnitude over 127); see zs_q8_save.  Matrices may be views with contiguous rows."""
-    p, rows, cols, ld = _matrix(x, _Q8_FORMATS, "x")
-    q, qr, qc, qld = _matrix(codes, _Q8_CODES, "codes")
-    _q8_shape("codes", (qr, qc), (rows, cols))
+    p, rows, cols, ld, fmt = _matrix(x, _Q8_FORMATS, "x")
+    q, qr, qc, qld, _ = _matrix(codes, _Q8_CODES, "codes")
+    if qr != rows or qc != cols:
+        _q8_shape("codes", qr, qc, rows, cols)
     s = _vector(scales, rows, "scales")
-    c = None if col_scale is None else _vector(col_scale, cols, "col_scale")
+    c, used = None, (x, codes, scales)
+    if col_scale is not None:
+        c, used = _vector(col_scale, cols, "col_scale"), (x, codes, scales, col_scale)
     if rule not in Q8_SCALES:
         raise ValueError(f"rule must be one of {tuple(Q8_SCALES)}, not {rule!r}")
-    _q8_call(_lib.zs_q8_save, "zs_q8_save", x, (codes, scales, col_scale),
-             (p, _Q8_FORMATS[x.dtype], ld, rows, cols, c, Q8_SCALES[rule], q, qld, s), stream)
+    _q8_call(_lib.zs_q8_save, "zs_q8_save", used, (p, fmt, ld, rows, cols, c, Q8_SCALES[rule], q, qld, s), stream)
 
 
 def q8_load(codes, scales, out, stream=None) -> None:
     """``out`` (bf16, fp16 or fp32) = ``codes`` times their rows' ``scales``; see zs_q8_load."""
-    q, rows, cols, qld = _matrix(codes, _Q8_CODES, "codes")
-    o, orows, ocols, old = _matrix(out, _Q8_FORMATS, "out")
-    _q8_shape("out", (orows, ocols), (rows, cols))
+    q, rows, cols, qld, _ = _matrix(codes, _Q8_CODES, "codes")
+    o, orows, ocols, old, fmt = _matrix(out, _Q8_FORMATS, "out")
+    if orows != rows or ocols != cols:
+        _q8_shape("out", orows, ocols, rows, cols)
     s = _vector(scales, rows, "scales")
-    _q8_call(_lib.zs_q8_load, "zs_q8_load", codes, (scales, out),
-             (q, qld, s, rows, cols, o, _Q8_FORMATS[out.dtype], old), stream)
+    _q8_call(_lib.zs_q8_load, "zs_q8_load", (codes, scales, out), (q, qld, s, rows, cols, o, fmt, old), stream)
 
 
 def q8_matmul(x_codes, x_scales, w_codes, w_scales, y, trans_w: bool = True, stream=None) -> None:
@@ -895,36 +903,44 @@ def q8_matmul(x_codes, x_scales, w_codes, w_scales, y, trans_w: bool = True, str
     is N x K.  ``trans_w``: x (T x K) times the weight's transpose, a linear layer's output (T x N); otherwise x
     (T x N) times the weight, its input gradient (T x K).  ``w_scales``: one for each column of ``y``, or None;
     see zs_q8_matmul."""
-    xp, T, inner, xld = _matrix(x_codes, _Q8_CODES, "x_codes")
-    wp, N, K, wld = _matrix(w_codes, _Q8_CODES, "w_codes")
-    yp, yr, yc, yld = _matrix(y, _Q8_FORMATS, "y")
-    _q8_shape("x_codes", (T, inner), (T, K if trans_w else N))
-    outer = N if trans_w else K
-    _q8_shape("y", (yr, yc), (T, outer))
+    xp, T, xc, xld, _ = _matrix(x_codes, _Q8_CODES, "x_codes")
+    wp, N, K, wld, _ = _matrix(w_codes, _Q8_CODES, "w_codes")
+    yp, yr, yc, yld, fmt = _matrix(y, _Q8_FORMATS, "y")
+    inner, outer = (K, N) if trans_w else (N, K)
+    if xc != inner:
+        _q8_shape("x_codes", T, xc, T, inner)
+    if yr != T or yc != outer:
+        _q8_shape("y", yr, yc, T, outer)
     sx = _vector(x_scales, T, "x_scales")
-    sw = None if w_scales is None else _vector(w_scales, outer, "w_scales")
-    _q8_call(_lib.zs_q8_matmul, "zs_q8_matmul", x_codes, (x_scales, w_codes, w_scales, y),
-             (xp, xld, sx, wp, wld, sw, T, N, K, 0 if trans_w else 1, yp, _Q8_FORMATS[y.dtype], yld), stream)
+    sw, used = None, (x_codes, x_scales, w_codes, y)
+    if w_scales is not None:
+        sw, used = _vector(w_scales, outer, "w_scales"), (x_codes, x_scales, w_codes, y, w_scales)
+    _q8_call(_lib.zs_q8_matmul, "zs_q8_matmul", used,
+             (xp, xld, sx, wp, wld, sw, T, N, K, 0 if trans_w else 1, yp, fmt, yld), stream)
 
 
 def q8_weight_grad(dy, x_codes, x_scales, dw, add=None, stream=None) -> None:
     """``dw`` (N x K; bf16, fp16 or fp32) = ``add`` + dy^T (x_codes * x_scales): a linear layer's weight gradient
     from the saved codes of its input (T x K) and its output gradient ``dy`` (T x N; bf16 or fp16).  ``add``: None,
     or a matrix with ``dw``'s dtype and row stride, ``dw`` itself among them; see zs_q8_weight_grad."""
-    dp, T, N, dld = _matrix(dy, _Q8_DY, "dy")
-    xp, xr, K, xld = _matrix(x_codes, _Q8_CODES, "x_codes")
-    _q8_shape("x_codes", (xr, K), (T, K))
-    wp, wr, wc, wld = _matrix(dw, _Q8_FORMATS, "dw")
-    _q8_shape("dw", (wr, wc), (N, K))
+    dp, T, N, dld, dfmt = _matrix(dy, _Q8_DY, "dy")
+    xp, xr, K, xld, _ = _matrix(x_codes, _Q8_CODES, "x_codes")
+    wp, wr, wc, wld, fmt = _matrix(dw, _Q8_FORMATS, "dw")
+    if xr != T:
+        _q8_shape("x_codes", xr, K, T, K)
+    if wr != N or wc != K:
+        _q8_shape("dw", wr, wc, N, K)
     s = _vector(x_scales, T, "x_scales")
-    ap = None
+    ap, used = None, (dy, x_codes, x_scales, dw)
     if add is not None:
-        ap, ar, ac, ald = _matrix(add, (dw.dtype,), "add")
-        _q8_shape("add", (ar, ac), (N, K))
+        ap, ar, ac, ald, _ = _matrix(add, {dw.dtype: fmt}, "add")
+        used = (dy, x_codes, x_scales, dw, add)
+        if ar != N or ac != K:
+            _q8_shape("add", ar, ac, N, K)
         if ald != wld and N > 1:
             raise ValueError(f"add has row stride {ald}, dw {wld}")
-    _q8_call(_lib.zs_q8_weight_grad, "zs_q8_weight_grad", dy, (x_codes, x_scales, dw, add),
-             (dp, _Q8_FORMATS[dy.dtype], dld, xp, xld, s, T, N, K, ap, wp, _Q8_FORMATS[dw.dtype], wld), stream)
+    _q8_call(_lib.zs_q8_weight_grad, "zs_q8_weight_grad", used,
+             (dp, dfmt, dld, xp, xld, s, T, N, K, ap, wp, fmt, wld), stream)
 
 
 # ------------------------------------------------------------ optimizer offload
