@@ -7,8 +7,9 @@
 //
 // Both are bound by memory: save reads each value once and writes a byte,
 // load reads a byte and writes a value.  A row is taken by 8 to 64 lanes of a
-// wave, or by a workgroup, that keep it in registers between the maximum and
-// the codes (rows of more than 16,384 columns are read twice).
+// wave, or by a workgroup, that keep it in registers, as it was stored,
+// between the maximum and the codes (rows of more than 16,384 columns are read
+// twice).
 #include "zs_q8_dev.h"
 
 namespace zs {
@@ -25,28 +26,23 @@ struct Raw8 {
 };
 
 template <int FMT>
-__device__ __forceinline__ void ld_raw(Raw8<FMT>& r, const void* row, int64_t col, int64_t cols) {
-  if (col + 8 <= cols) {
-    if constexpr (FMT == kFP32) {
-      const u32x4 a = ld_any<u32x4>((const float*)row + col), b = ld_any<u32x4>((const float*)row + col + 4);
+__device__ __forceinline__ void ld_raw(Raw8<FMT>& r, const void* row, int64_t col) {
+  if constexpr (FMT == kFP32) {
+    const u32x4 a = ld_any<u32x4>((const float*)row + col), b = ld_any<u32x4>((const float*)row + col + 4);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) r.w[k] = a[k], r.w[4 + k] = b[k];
-    } else {
-      const u32x4 a = ld_any<u32x4>((const uint16_t*)row + col);
+    for (int k = 0; k < 4; ++k) r.w[k] = a[k], r.w[4 + k] = b[k];
+  } else {
+    const u32x4 a = ld_any<u32x4>((const uint16_t*)row + col);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) r.w[k] = a[k];
-    }
-    return;
+    for (int k = 0; k < 4; ++k) r.w[k] = a[k];
   }
+}
+// Forgets what was made of the words: they are taken apart again where they
+// are needed next, instead of held in twice the registers.
+template <int FMT>
+__device__ __forceinline__ void keep_raw(Raw8<FMT>& r) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if constexpr (FMT == kFP32) {
-      r.w[k] = col + k < cols ? ((const GLB uint32_t*)row)[col + k] : 0u;
-    } else {
-      const uint32_t h = col + k < cols ? ((const GLB uint16_t*)row)[col + k] : 0u;
-      r.w[k / 2] = k % 2 ? r.w[k / 2] | (h << 16) : h;
-    }
-  }
+  for (uint32_t& w : r.w) asm volatile("" : "+v"(w));
 }
 
 template <int FMT>
@@ -60,19 +56,13 @@ __device__ __forceinline__ float raw_value(const Raw8<FMT>& r, int k) {
 // The eight values of a chunk, times their columns' factors (one fp32
 // rounding each).
 template <int FMT, bool COL>
-__device__ __forceinline__ void values(const Raw8<FMT>& r, const float* col_scale, int64_t col, int64_t cols,
-                                       float* v) {
+__device__ __forceinline__ void values(const Raw8<FMT>& r, const float* col_scale, int64_t col, float* v) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) v[k] = raw_value<FMT>(r, k);
   if constexpr (COL) {
-    if (col + 8 <= cols) {
-      const f32x4 a = ld_any<f32x4>(col_scale + col), b = ld_any<f32x4>(col_scale + col + 4);
+    const f32x4 a = ld_any<f32x4>(col_scale + col), b = ld_any<f32x4>(col_scale + col + 4);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = v[k] * a[k], v[4 + k] = v[4 + k] * b[k];
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = col + k < cols ? v[k] * col_scale[col + k] : 0.0f;
-    }
+    for (int k = 0; k < 4; ++k) v[k] = v[k] * a[k], v[4 + k] = v[4 + k] * b[k];
   }
 }
 
@@ -80,15 +70,40 @@ __device__ __forceinline__ void values(const Raw8<FMT>& r, const float* col_scal
 // every finite value, so a plain integer maximum also finds those.
 __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// The largest magnitude met so far, as bits: two 16-bit ones side by side
+// where the values are 16-bit and have no factors, else one of fp32.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+template <int FMT, bool COL>
+__device__ __forceinline__ uint32_t larger(uint32_t top, const Raw8<FMT>& r, const float* col_scale, int64_t col) {
+  if constexpr (FMT != kFP32 && !COL) {
+    u16x2 t = __builtin_bit_cast(u16x2, top);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t = __builtin_elementwise_max(t, __builtin_bit_cast(u16x2, r.w[k] & 0x7FFF7FFFu));
+    return __builtin_bit_cast(uint32_t, t);
+  } else {
+    float v[8];
+    values<FMT, COL>(r, col_scale, col, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, mag(v[k]));
+    return top;
+  }
+}
+template <int FMT, bool COL>
+__device__ __forceinline__ uint32_t largest(uint32_t top) {
+  if constexpr (FMT != kFP32 && !COL) return mag(h_one<FMT>((uint16_t)max(top & 0xFFFFu, top >> 16)));
+  return top;
+}
+
 struct Scale {
   float s, inv;  // the scale, and 1 / s
   bool bad;      // the row holds a NaN or an infinity
 };
 
-__device__ __forceinline__ Scale scale_of(uint32_t top, int rule) {
+template <bool POW2>
+__device__ __forceinline__ Scale scale_of(uint32_t top) {
   Scale r;
   r.bad = top >= 0x7F800000u;
-  if (rule == ZS_Q8_SCALE_POW2) {
+  if constexpr (POW2) {
     // 127 = 1.984375 * 2^6: one power of two more when the mantissa is above that
     const int32_t e = (int32_t)(top >> 23) - 6 + ((top & 0x7FFFFFu) > 0x7E0000u ? 1 : 0);
     const int32_t b = r.bad || e < 1 ? 1 : e;
@@ -108,7 +123,8 @@ __device__ __forceinline__ Scale scale_of(uint32_t top, int rule) {
 // a half.  Those values, about one in 30,000, are decided by the
 // remainder v - q s, which a fused multiply-add gives exactly.  With a power of
 // two the product is exact and nothing needs deciding.
-__device__ __forceinline__ u32x2 codes8(const float* v, const Scale& sc, int rule) {
+template <bool POW2>
+__device__ __forceinline__ u32x2 codes8(const float* v, const Scale& sc) {
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
   float m[8];
   float far = 0.0f;
@@ -116,16 +132,17 @@ __device__ __forceinline__ u32x2 codes8(const float* v, const Scale& sc, int rul
   for (int k = 0; k < 8; ++k) {
     const float t = v[k] * sc.inv;
     m[k] = t + kMagic;
-    far = fmaxf(far, fabsf(t - (m[k] - kMagic)));
+    if constexpr (!POW2) far = fmaxf(far, fabsf(t - (m[k] - kMagic)));
   }
-  if (rule != ZS_Q8_SCALE_POW2 && far > 0.49998f) {
+  if constexpr (!POW2) {
+    if (far > 0.49998f) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float q = m[k] - kMagic;
-      const float r = __builtin_fmaf(-q, sc.s, v[k]);
-      const float two = 2.0f * fabsf(r);
-      const bool odd = (__float_as_uint(m[k]) & 1u) != 0;
-      if (two > sc.s || (two == sc.s && odd)) m[k] = m[k] + (r > 0.0f ? 1.0f : -1.0f);
+      for (int k = 0; k < 8; ++k) {
+        const float r = __builtin_fmaf(-(m[k] - kMagic), sc.s, v[k]);
+        const float two = 2.0f * fabsf(r);
+        const bool odd = (__float_as_uint(m[k]) & 1u) != 0;
+        m[k] = m[k] + (two > sc.s || (two == sc.s && odd) ? __builtin_copysignf(1.0f, r) : 0.0f);
+      }
     }
   }
   u32x2 w;
@@ -139,57 +156,54 @@ __device__ __forceinline__ u32x2 codes8(const float* v, const Scale& sc, int rul
   return w;
 }
 
-__device__ __forceinline__ void st_codes(int8_t* row, int64_t col, int64_t cols, u32x2 w) {
-  if (col + 8 <= cols) {
-    st_any<u32x2>(row + col, w);
-    return;
-  }
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (col + k < cols) ((GLB int8_t*)row)[col + k] = (int8_t)(w[k / 4] >> (8 * (k % 4)));
-}
-
-// lanes: lanes per row, a power of two from 8 to 64, or kRowBlock (one row per
-// workgroup).  HELD: chunks of 8 values a lane keeps (lanes * HELD * 8 >= cols),
-// or 0 to read the row twice.
-template <int FMT, bool COL, int HELD>
+// Rows of at least 8 columns.  lanes: lanes per row, a power of two from 8 to
+// 64, or kRowBlock (one row per workgroup).  HELD: chunks of 8 values a lane
+// keeps (lanes * HELD * 8 >= cols), or 0 to read the row twice.  The last chunk
+// of a row ends with it and may take some of the one before again, and lanes
+// past the last row take that again: the same codes to the same places.
+template <int FMT, bool COL, bool POW2, int HELD>
 __global__ __launch_bounds__(kRowBlock) void q8_save_kernel(const Q8Save a, int lanes) {
   __shared__ uint32_t wave_top[kRowBlock / 64];
   const int lane = threadIdx.x & (lanes - 1);
   const int sub = threadIdx.x / lanes, per = kRowBlock / lanes;
+  const int64_t cols = a.cols;
   for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < a.rows; r0 += (int64_t)gridDim.x * per) {
-    const int64_t row = r0 + sub;
-    const bool live = row < a.rows;  // every lane stays for the reductions
-    const int64_t cols = live ? a.cols : 0;
+    const int64_t row = r0 + sub < a.rows ? r0 + sub : a.rows - 1;
     constexpr int kBytes = FMT == kFP32 ? 4 : 2;
-    const char* x = (const char*)a.x + (live ? row : 0) * a.ld_x * kBytes;
-    int8_t* q = a.codes + (live ? row : 0) * a.ld_codes;
+    const char* x = (const char*)a.x + row * a.ld_x * kBytes;
+    int8_t* q = a.codes + row * a.ld_codes;
     uint32_t top = 0;
     Raw8<FMT> held[HELD > 0 ? HELD : 1];
-    float v[8];
+    const auto at = [&](int64_t chunk) { return chunk * 8 + 8 <= cols ? chunk * 8 : cols - 8; };
+    // with factors: the products, so that the factors are read once
+    Raw8<kFP32> products[COL && HELD > 0 ? HELD : 1];
     if constexpr (HELD > 0) {
 #pragma unroll
-      for (int i = 0; i < HELD; ++i) {
-        const int64_t col = (int64_t)(lane + i * lanes) * 8;
-        if (col < cols) ld_raw<FMT>(held[i], x, col, cols);
-      }
+      for (int i = 0; i < HELD; ++i)
+        if ((int64_t)(lane + i * lanes) * 8 < cols) ld_raw<FMT>(held[i], x, at(lane + i * lanes));
 #pragma unroll
       for (int i = 0; i < HELD; ++i) {
-        const int64_t col = (int64_t)(lane + i * lanes) * 8;
-        if (col < cols) {
-          values<FMT, COL>(held[i], a.col_scale, col, cols, v);
+        if ((int64_t)(lane + i * lanes) * 8 < cols) {
+          if constexpr (COL) {
+            float v[8];
+            values<FMT, true>(held[i], a.col_scale, at(lane + i * lanes), v);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) top = max(top, mag(v[k]));
+            for (int k = 0; k < 8; ++k) {
+              products[i].w[k] = __float_as_uint(v[k]);
+              top = max(top, mag(v[k]));
+            }
+          } else {
+            top = larger<FMT, false>(top, held[i], nullptr, 0);
+          }
         }
       }
     } else {
-      for (int64_t col = (int64_t)lane * 8; col < cols; col += (int64_t)lanes * 8) {
-        ld_raw<FMT>(held[0], x, col, cols);
-        values<FMT, COL>(held[0], a.col_scale, col, cols, v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = max(top, mag(v[k]));
+      for (int64_t c = lane; c * 8 < cols; c += lanes) {
+        ld_raw<FMT>(held[0], x, at(c));
+        top = larger<FMT, COL>(top, held[0], a.col_scale, at(c));
       }
     }
+    top = largest<FMT, COL>(top);
     for (int off = (lanes < 64 ? lanes : 64) / 2; off >= 1; off >>= 1)
       top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
     if (lanes == kRowBlock) {
@@ -198,24 +212,55 @@ __global__ __launch_bounds__(kRowBlock) void q8_save_kernel(const Q8Save a, int 
       top = max(max(wave_top[0], wave_top[1]), max(wave_top[2], wave_top[3]));
       __syncthreads();
     }
-    const Scale sc = scale_of(top, a.rule);
-    if (live && lane == 0) ((GLB float*)a.scales)[row] = sc.s;
+    const Scale sc = scale_of<POW2>(top);
+    if (lane == 0) ((GLB float*)a.scales)[row] = sc.s;
+    float v[8];
     if constexpr (HELD > 0) {
 #pragma unroll
       for (int i = 0; i < HELD; ++i) {
-        const int64_t col = (int64_t)(lane + i * lanes) * 8;
-        if (col < cols) {
-          values<FMT, COL>(held[i], a.col_scale, col, cols, v);
-          st_codes(q, col, cols, codes8(v, sc, a.rule));
+        if ((int64_t)(lane + i * lanes) * 8 < cols) {
+          const int64_t col = at(lane + i * lanes);
+          if constexpr (COL) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(products[i].w[k]);
+          } else {
+            keep_raw<FMT>(held[i]);
+            values<FMT, false>(held[i], nullptr, col, v);
+          }
+          st_any<u32x2>(q + col, codes8<POW2>(v, sc));
         }
       }
     } else {
-      for (int64_t col = (int64_t)lane * 8; col < cols; col += (int64_t)lanes * 8) {
-        ld_raw<FMT>(held[0], x, col, cols);
-        values<FMT, COL>(held[0], a.col_scale, col, cols, v);
-        st_codes(q, col, cols, codes8(v, sc, a.rule));
+      for (int64_t c = lane; c * 8 < cols; c += lanes) {
+        ld_raw<FMT>(held[0], x, at(c));
+        values<FMT, COL>(held[0], a.col_scale, at(c), v);
+        st_any<u32x2>(q + at(c), codes8<POW2>(v, sc));
       }
     }
+  }
+}
+
+// Rows of fewer than 8 columns: a thread each.
+template <int FMT, bool POW2>
+__global__ __launch_bounds__(kRowBlock) void q8_save_narrow_kernel(const Q8Save a) {
+  for (int64_t row = (int64_t)blockIdx.x * kRowBlock + threadIdx.x; row < a.rows; row += (int64_t)gridDim.x * kRowBlock) {
+    float v[8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      v[k] = 0.0f;
+      if (k < a.cols) {
+        v[k] = ld_elem<FMT>(a.x, row * a.ld_x + k);
+        if (a.col_scale != nullptr) v[k] = v[k] * ((const GLB float*)a.col_scale)[k];
+      }
+      top = max(top, mag(v[k]));
+    }
+    const Scale sc = scale_of<POW2>(top);
+    ((GLB float*)a.scales)[row] = sc.s;
+    const u32x2 w = codes8<POW2>(v, sc);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < a.cols) ((GLB int8_t*)a.codes)[row * a.ld_codes + k] = (int8_t)(w[k / 4] >> (8 * (k % 4)));
   }
 }
 
@@ -250,21 +295,41 @@ __global__ __launch_bounds__(kRowBlock) void q8_load_kernel(const Q8Load a, int 
   }
 }
 
-template <int FMT, bool COL>
+dim3 row_grid(int64_t rows, int64_t per) {
+  const int64_t groups = (rows + per - 1) / per;
+  return dim3((unsigned)(groups < (1 << 20) ? groups : (1 << 20)));
+}
+
+template <int FMT, bool COL, bool POW2>
 hipError_t save_launch(const Q8Save& a, hipStream_t stream) {
   const int64_t chunks = (a.cols + 7) / 8;
   int lanes = 8;
   while (lanes < 64 && chunks > lanes * 4) lanes *= 2;
   if (chunks > lanes * 4) lanes = kRowBlock;
-  const int64_t per = kRowBlock / lanes, groups = (a.rows + per - 1) / per;
-  const dim3 grid((unsigned)(groups < (1 << 20) ? groups : (1 << 20)));
-  if (chunks <= (int64_t)lanes * 4)
-    q8_save_kernel<FMT, COL, 4><<<grid, kRowBlock, 0, stream>>>(a, lanes);
+  const dim3 grid = row_grid(a.rows, kRowBlock / lanes);
+  if (chunks <= (int64_t)lanes * 2)
+    q8_save_kernel<FMT, COL, POW2, 2><<<grid, kRowBlock, 0, stream>>>(a, lanes);
+  else if (chunks <= (int64_t)lanes * 4)
+    q8_save_kernel<FMT, COL, POW2, 4><<<grid, kRowBlock, 0, stream>>>(a, lanes);
   else if (chunks <= (int64_t)lanes * 8)
-    q8_save_kernel<FMT, COL, 8><<<grid, kRowBlock, 0, stream>>>(a, lanes);
+    q8_save_kernel<FMT, COL, POW2, 8><<<grid, kRowBlock, 0, stream>>>(a, lanes);
   else
-    q8_save_kernel<FMT, COL, 0><<<grid, kRowBlock, 0, stream>>>(a, lanes);
+    q8_save_kernel<FMT, COL, POW2, 0><<<grid, kRowBlock, 0, stream>>>(a, lanes);
   return hipGetLastError();
+}
+template <int FMT>
+hipError_t save_launch(const Q8Save& a, hipStream_t stream) {
+  const bool pow2 = a.rule == ZS_Q8_SCALE_POW2;
+  if (a.cols < 8) {
+    const dim3 grid = row_grid(a.rows, kRowBlock);
+    if (pow2)
+      q8_save_narrow_kernel<FMT, true><<<grid, kRowBlock, 0, stream>>>(a);
+    else
+      q8_save_narrow_kernel<FMT, false><<<grid, kRowBlock, 0, stream>>>(a);
+    return hipGetLastError();
+  }
+  if (a.col_scale) return pow2 ? save_launch<FMT, true, true>(a, stream) : save_launch<FMT, true, false>(a, stream);
+  return pow2 ? save_launch<FMT, false, true>(a, stream) : save_launch<FMT, false, false>(a, stream);
 }
 
 template <int FMT>
@@ -272,9 +337,7 @@ hipError_t load_launch(const Q8Load& a, hipStream_t stream) {
   const int64_t chunks = (a.cols + 7) / 8;
   int lanes = 4;
   while (lanes < kRowBlock && chunks > lanes) lanes *= 2;
-  const int64_t per = kRowBlock / lanes, groups = (a.rows + per - 1) / per;
-  const dim3 grid((unsigned)(groups < (1 << 20) ? groups : (1 << 20)));
-  q8_load_kernel<FMT><<<grid, kRowBlock, 0, stream>>>(a, lanes);
+  q8_load_kernel<FMT><<<row_grid(a.rows, kRowBlock / lanes), kRowBlock, 0, stream>>>(a, lanes);
   return hipGetLastError();
 }
 
@@ -282,9 +345,9 @@ hipError_t load_launch(const Q8Load& a, hipStream_t stream) {
 
 hipError_t launch_q8_save(const Q8Save& a, hipStream_t stream) {
   switch (a.format) {
-    case ZS_FORMAT_BF16: return a.col_scale ? save_launch<kBF16, true>(a, stream) : save_launch<kBF16, false>(a, stream);
-    case ZS_FORMAT_FP16: return a.col_scale ? save_launch<kFP16, true>(a, stream) : save_launch<kFP16, false>(a, stream);
-    default: return a.col_scale ? save_launch<kFP32, true>(a, stream) : save_launch<kFP32, false>(a, stream);
+    case ZS_FORMAT_BF16: return save_launch<kBF16>(a, stream);
+    case ZS_FORMAT_FP16: return save_launch<kFP16>(a, stream);
+    default: return save_launch<kFP32>(a, stream);
   }
 }
 
