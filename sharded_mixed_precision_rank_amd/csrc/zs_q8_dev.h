@@ -29,6 +29,12 @@ __device__ __forceinline__ void st_any(E* p, V v) {
   typedef V U __attribute__((aligned(__alignof__(E))));
   *(GLB U*)(GLB E*)p = v;
 }
+// The same past the caches' normal order: for outputs much larger than them.
+template <class V, class E>
+__device__ __forceinline__ void st_past(E* p, V v) {
+  typedef V U __attribute__((aligned(__alignof__(E))));
+  __builtin_nontemporal_store(v, (GLB U*)(GLB E*)p);
+}
 
 // Element i of an array in storage format FMT, as fp32.
 template <int FMT>

@@ -65,60 +65,68 @@ __device__ __forceinline__ void fp16_parts(u32x4 h, u32x4& hi, u32x4& lo) {
   }
 }
 
-// Four results at row m, columns n .. n + 3 (those below N), any format.
-template <int FMT>
-__device__ __forceinline__ void store_row4(const Q8Gemm& a, int64_t m, int64_t n, float* v, bool adds) {
-  const int64_t i = m * a.ldd + n;
-  if (adds) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (n + r < a.N) v[r] = ld_elem<FMT>(a.add, i + r) + v[r];
-  }
-  if (n + 4 <= a.N) {
-    st_four<FMT>(a.d, i, v);
-  } else {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (n + r < a.N) st_elem<FMT>(a.d, i + r, v[r]);
-  }
-}
-__device__ __forceinline__ void store4(const Q8Gemm& a, int64_t m, int64_t n, float* v, bool adds) {
-  if (a.format == ZS_FORMAT_BF16)
-    store_row4<kBF16>(a, m, n, v, adds);
-  else if (a.format == ZS_FORMAT_FP16)
-    store_row4<kFP16>(a, m, n, v, adds);
-  else
-    store_row4<kFP32>(a, m, n, v, adds);
-}
-
-// RUN results at row m from column n on (those below N).
-template <int FMT, int RUN>
-__device__ __forceinline__ void store_run_as(const Q8Gemm& a, int64_t m, int64_t n, const float* v) {
+// RUN (4 or 8) results at row m from column n on (those below N), plus what
+// add holds there.  PAST: written past the caches.  The products of the large
+// tiles are: their outputs otherwise push the operands out (8192 x 11008 x 4096
+// 314 us against 361, 8192 x 4096 x 4096 122 against 136, kNN 115 against 125;
+// weight gradients, smaller beside their operands, gain 1% or lose 2%).
+template <int FMT, int RUN, bool PAST>
+__device__ __forceinline__ void store_run_as(const Q8Gemm& a, int64_t m, int64_t n, float* v) {
   const int64_t i = m * a.ldd + n;
   if (n + RUN <= a.N) {
-    if constexpr (FMT == kFP32 || RUN < 8) {
+    if (a.add != nullptr) {
 #pragma unroll
-      for (int r = 0; r < RUN; r += 4) st_four<FMT>(a.d, i + r, v + r);
+      for (int r = 0; r < RUN; r += 4) {
+        if constexpr (FMT == kFP32) {
+          const f32x4 x = ld_any<f32x4>((const float*)a.add + i + r);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[r + k] = x[k] + v[r + k];
+        } else {
+          const u32x2 x = ld_any<u32x2>((const uint16_t*)a.add + i + r);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[r + k] = (k % 2 ? h_hi<FMT>(x[k / 2]) : h_lo<FMT>(x[k / 2])) + v[r + k];
+        }
+      }
+    }
+    if constexpr (FMT == kFP32) {
+#pragma unroll
+      for (int r = 0; r < RUN; r += 4) {
+        const f32x4 w = {v[r], v[r + 1], v[r + 2], v[r + 3]};
+        PAST ? st_past((float*)a.d + i + r, w) : st_any((float*)a.d + i + r, w);
+      }
+    } else if constexpr (RUN == 8) {
+      const u32x4 w = {pack_two<FMT>(v[0], v[1]), pack_two<FMT>(v[2], v[3]), pack_two<FMT>(v[4], v[5]),
+                       pack_two<FMT>(v[6], v[7])};
+      PAST ? st_past((uint16_t*)a.d + i, w) : st_any((uint16_t*)a.d + i, w);
     } else {
-#pragma unroll
-      for (int r = 0; r < RUN; r += 8)
-        st_any<u32x4>((uint16_t*)a.d + i + r, (u32x4){pack_two<FMT>(v[r], v[r + 1]), pack_two<FMT>(v[r + 2], v[r + 3]),
-                                                      pack_two<FMT>(v[r + 4], v[r + 5]), pack_two<FMT>(v[r + 6], v[r + 7])});
+      st_four<FMT>(a.d, i, v);
     }
   } else {
 #pragma unroll
-    for (int r = 0; r < RUN; ++r)
-      if (n + r < a.N) st_elem<FMT>(a.d, i + r, v[r]);
+    for (int r = 0; r < RUN; ++r) {
+      if (n + r < a.N) st_elem<FMT>(a.d, i + r, a.add != nullptr ? ld_elem<FMT>(a.add, i + r) + v[r] : v[r]);
+    }
   }
 }
-template <int RUN>
-__device__ __forceinline__ void store_run(const Q8Gemm& a, int64_t m, int64_t n, const float* v) {
+template <int RUN, bool PAST = false>
+__device__ __forceinline__ void store_run(const Q8Gemm& a, int64_t m, int64_t n, float* v) {
   if (a.format == ZS_FORMAT_BF16)
-    store_run_as<kBF16, RUN>(a, m, n, v);
+    store_run_as<kBF16, RUN, PAST>(a, m, n, v);
   else if (a.format == ZS_FORMAT_FP16)
-    store_run_as<kFP16, RUN>(a, m, n, v);
+    store_run_as<kFP16, RUN, PAST>(a, m, n, v);
   else
-    store_run_as<kFP32, RUN>(a, m, n, v);
+    store_run_as<kFP32, RUN, PAST>(a, m, n, v);
+}
+
+// Two accumulators side by side (columns 4 g + r of one 16-column fragment and
+// of the next), traded between lane groups so that a lane has 8 consecutive
+// columns: those from eight_at(g) on of the 32.
+__device__ __forceinline__ int eight_at(int g) { return (g & 1) * 16 + (g >> 1) * 8; }
+__device__ __forceinline__ void trade(uint32_t x, uint32_t y, uint32_t& lo, uint32_t& hi) {
+  typedef uint32_t Two __attribute__((ext_vector_type(2)));
+  const Two t = __builtin_bit_cast(Two, __builtin_amdgcn_permlane16_swap(x, y, false, false));
+  lo = t[0];
+  hi = t[1];
 }
 
 // ---------------------------------------------------------------------------
@@ -263,7 +271,7 @@ __global__ __launch_bounds__(256) void q8_gemm_any(const Q8Gemm a, int64_t tiles
           v[r] = kT ? accf[i][j][r] : (float)acci[i][j][r] * rs;
           if (!kT && a.cs != nullptr && n + r < a.N) v[r] = v[r] * ((const GLB float*)a.cs)[n + r];
         }
-        if (n < a.N) store4(a, m, n, v, kT && a.add != nullptr);
+        if (n < a.N) store_run<4>(a, m, n, v);
       }
     }
     __syncthreads();  // before the next tile's first pieces are written
@@ -384,7 +392,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
   constexpr int kGroup = 16 * BN + (BN > 64 ? 128 : 0);
   constexpr int kABytes = BM * kStage, kBBytes = kNT ? BN * kStage : kStage / 16 * kGroup, kBuf = kABytes + kBBytes;
   constexpr int kALoads = kABytes / 1024 / kWaves, kBLoads = BN * kStage / 1024 / kWaves;
-  static_assert(FN % 4 == 0 && kALoads > 0 && kBLoads > 0 && (NS & (NS - 1)) == 0, "tile shape");
+  static_assert(FN % 2 == 0 && kBLoads % 2 == 0 && kALoads > 0 && kBLoads > 0 && (NS & (NS - 1)) == 0, "tile shape");
   __shared__ __attribute__((aligned(1024))) char lds[NS * kBuf];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, i16 = lane & 15;
@@ -405,8 +413,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
   const uint32_t va = (uint32_t)(lane >> 3) * lda + (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);
   uint32_t vb[2];
   if constexpr (kNT) {
-    // a fragment's row i16 is column (i16 / 4) * 16 + 4 j + i16 % 4 of its 64, which leaves each lane 16
-    // consecutive columns of the result; so s(r) = r % 4 + 4 (r / 16 % 2)
+    // a fragment's row i16 is column (i16 / 4) * 8 + 4 (j % 2) + i16 % 4 of the 32 of two fragments, which leaves each
+    // lane 8 consecutive columns of the result; so s(r) = r % 4 + 4 (r / 8 % 2)
 #pragma unroll
     for (int p = 0; p < 2; ++p)
       vb[p] = (uint32_t)(lane >> 3) * ldb + (uint32_t)(((lane & 7) ^ ((lane >> 3 & 3) | p << 2)) * 16);
@@ -433,7 +441,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
     const int t = wave * kBLoads + j;
     const uint32_t to = lds0 + (stage & (NS - 1)) * kBuf + kABytes;
     if constexpr (kNT) {
-      load_to_lds(rb_nt, vb[t >> 1 & 1] + (uint32_t)(t * 8) * ldb + from(stage), to + t * 1024);
+      load_to_lds(rb_nt, vb[t & 1] + (uint32_t)(t * 8) * ldb + from(stage), to + t * 1024);
     } else {
       constexpr int kRows = 64 / (BN / 16);
       const int32_t k0 = stage * kStage;
@@ -451,14 +459,14 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
 
   const int s7 = i16 & 7;
   const int at_a = (wm + i16) * kStage;
-  const int at_b_nt = kABytes + (wn + (i16 >> 2) * 16 + (i16 & 3)) * kStage;
+  const int at_b_nt = kABytes + (wn + (i16 >> 2) * 8 + (i16 & 3)) * kStage;
   const int at_b_nn = kABytes + g * kGroup + (i16 >> 1) * BN + (i16 & 1) * 8;
   auto read_a = [&](int buf, int half, int i) {
     fa[half][i] = *(const LDS i32x4*)((LDS char*)lds + buf * kBuf + at_a + i * 16 * kStage + ((4 * half + g) ^ s7) * 16);
   };
   auto read_b = [&](int buf, int half, int j) {
     if constexpr (kNT) {
-      fb[half][j] = *(const LDS i32x4*)((LDS char*)lds + buf * kBuf + at_b_nt + (j / 4 * 64 + j % 4 * 4) * kStage +
+      fb[half][j] = *(const LDS i32x4*)((LDS char*)lds + buf * kBuf + at_b_nt + (j / 2 * 32 + j % 2 * 4) * kStage +
                                         ((4 * half + g) ^ s7) * 16);
     } else {
       // rows r and r + 8 share s
@@ -536,8 +544,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way to LDS when the workgroup ends
   }
 
-  // Results: lane i16 holds row i16 of a fragment, kRun consecutive columns from its accumulators.
-  constexpr int kRun = kNT ? 16 : 4;
+  // Results: lane i16 holds row i16 of a fragment, 8 consecutive columns from two accumulators (kNN: after a trade),
+  // so that a store covers 64 bytes of each of 16 rows (with 4 columns a lane, kNN took 4-20% longer: 148 us against 120
+  // at 8192 x 4096 x 4096).
+  constexpr int kRun = 8;
   float rs[FM];
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -546,7 +556,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
   }
 #pragma unroll
   for (int c = 0; c < FN * 4 / kRun; ++c) {
-    const int64_t n = n0 + wn + (kNT ? c * 64 + g * 16 : c * 16 + g * 4);
+    const int64_t n = n0 + wn + c * 32 + (kNT ? g * 8 : eight_at(g));
     float cs[kRun];
     if (a.cs != nullptr) {
 #pragma unroll
@@ -555,13 +565,26 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
       const int64_t m = m0 + wm + i * 16 + i16;
+      int32_t sum[kRun];
+      if constexpr (kNT) {
+#pragma unroll
+        for (int r = 0; r < kRun; ++r) sum[r] = acc[i][2 * c + r / 4][r % 4];
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          uint32_t lo, hi;
+          trade((uint32_t)acc[i][2 * c][r], (uint32_t)acc[i][2 * c + 1][r], lo, hi);
+          sum[r] = (int32_t)lo;
+          sum[4 + r] = (int32_t)hi;
+        }
+      }
       float v[kRun];
 #pragma unroll
       for (int r = 0; r < kRun; ++r) {
-        v[r] = (float)acc[i][c * kRun / 4 + r / 4][r % 4] * rs[i];
+        v[r] = (float)sum[r] * rs[i];
         if (a.cs != nullptr) v[r] = v[r] * cs[r];
       }
-      if (m < a.M) store_run<kRun>(a, m, n, v);
+      if (m < a.M && n < a.N) store_run<kRun, (BM * BN > 64 * 64)>(a, m, n, v);
     }
   }
 }
@@ -712,7 +735,7 @@ __global__ __launch_bounds__(W * 64, 2) void q8_gemm_split(const Q8Gemm a, uint3
       v[r] = (float)sums[row * kPitch + (four / 4 * 4 + r) * 4 + four % 4] * rs;
       if (a.cs != nullptr && n + r < a.N) v[r] = v[r] * ((const GLB float*)a.cs)[n + r];
     }
-    store4(a, m, n, v, false);
+    store_run<4>(a, m, n, v);
   }
 }
 
@@ -1009,12 +1032,18 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_grad_tile(const Q8Gemm a, u
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int64_t m = m0 + wm + i * 16 + i16;
-    if (m >= a.M) continue;
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int64_t n = n0 + wn + j * 16 + g * 4;
-      float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-      if (n < a.N) store4(a, m, n, v, a.add != nullptr);
+    for (int j = 0; j < FN; j += 2) {
+      float v[8];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        uint32_t lo, hi;
+        trade(__float_as_uint(acc[i][j][r]), __float_as_uint(acc[i][j + 1][r]), lo, hi);
+        v[r] = __uint_as_float(lo);
+        v[4 + r] = __uint_as_float(hi);
+      }
+      const int64_t n = n0 + wn + j * 16 + eight_at(g);
+      if (m < a.M && n < a.N) store_run<8>(a, m, n, v);
     }
   }
 }
