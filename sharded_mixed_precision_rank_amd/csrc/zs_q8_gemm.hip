@@ -66,12 +66,10 @@ __device__ __forceinline__ void fp16_parts(u32x4 h, u32x4& hi, u32x4& lo) {
 }
 
 // RUN (4 or 8) results at row m from column n on (those below N), plus what
-// add holds there.  PAST: written past the caches.  The products of the large
-// tiles are: their outputs otherwise push the operands out (8192 x 11008 x 4096
-// 314 us against 361, 8192 x 4096 x 4096 122 against 136, kNN 115 against 125;
-// weight gradients, smaller beside their operands, gain 1% or lose 2%).
-template <int FMT, int RUN, bool PAST>
-__device__ __forceinline__ void store_run_as(const Q8Gemm& a, int64_t m, int64_t n, float* v) {
+// add holds there; past: around the caches, where those are whole 64-byte
+// pieces.
+template <int FMT, int RUN>
+__device__ __forceinline__ void store_run_as(const Q8Gemm& a, int64_t m, int64_t n, float* v, bool past) {
   const int64_t i = m * a.ldd + n;
   if (n + RUN <= a.N) {
     if (a.add != nullptr) {
@@ -90,14 +88,14 @@ __device__ __forceinline__ void store_run_as(const Q8Gemm& a, int64_t m, int64_t
     }
     if constexpr (FMT == kFP32) {
 #pragma unroll
-      for (int r = 0; r < RUN; r += 4) {
-        const f32x4 w = {v[r], v[r + 1], v[r + 2], v[r + 3]};
-        PAST ? st_past((float*)a.d + i + r, w) : st_any((float*)a.d + i + r, w);
-      }
+      for (int r = 0; r < RUN; r += 4) st_four<FMT>(a.d, i + r, v + r);
     } else if constexpr (RUN == 8) {
       const u32x4 w = {pack_two<FMT>(v[0], v[1]), pack_two<FMT>(v[2], v[3]), pack_two<FMT>(v[4], v[5]),
                        pack_two<FMT>(v[6], v[7])};
-      PAST ? st_past((uint16_t*)a.d + i, w) : st_any((uint16_t*)a.d + i, w);
+      if (past)
+        st_past((uint16_t*)a.d + i, w);
+      else
+        st_any((uint16_t*)a.d + i, w);
     } else {
       st_four<FMT>(a.d, i, v);
     }
@@ -108,14 +106,14 @@ __device__ __forceinline__ void store_run_as(const Q8Gemm& a, int64_t m, int64_t
     }
   }
 }
-template <int RUN, bool PAST = false>
-__device__ __forceinline__ void store_run(const Q8Gemm& a, int64_t m, int64_t n, float* v) {
+template <int RUN>
+__device__ __forceinline__ void store_run(const Q8Gemm& a, int64_t m, int64_t n, float* v, bool past = false) {
   if (a.format == ZS_FORMAT_BF16)
-    store_run_as<kBF16, RUN, PAST>(a, m, n, v);
+    store_run_as<kBF16, RUN>(a, m, n, v, past);
   else if (a.format == ZS_FORMAT_FP16)
-    store_run_as<kFP16, RUN, PAST>(a, m, n, v);
+    store_run_as<kFP16, RUN>(a, m, n, v, past);
   else
-    store_run_as<kFP32, RUN, PAST>(a, m, n, v);
+    store_run_as<kFP32, RUN>(a, m, n, v, past);
 }
 
 // Two accumulators side by side (columns 4 g + r of one 16-column fragment and
@@ -320,6 +318,14 @@ __device__ __forceinline__ int32_t left_of(int64_t total, int64_t done, int32_t 
 // (vmcnt) before anyone reads them, and before the workgroup ends.
 __device__ __forceinline__ void load_to_lds(Rsrc rsrc, uint32_t voff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :
+               : "v"(voff), "s"(rsrc), "s"(lds)
+               : "memory");
+}
+
+// The same with 4 bytes a lane.
+__device__ __forceinline__ void load4_to_lds(Rsrc rsrc, uint32_t voff, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
                :
                : "v"(voff), "s"(rsrc), "s"(lds)
                : "memory");
@@ -548,6 +554,10 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
   // so that a store covers 64 bytes of each of 16 rows (with 4 columns a lane, kNN took 4-20% longer: 148 us against 120
   // at 8192 x 4096 x 4096).
   constexpr int kRun = 8;
+  // Large 16-bit outputs otherwise push the operands out of the caches (8192 x 11008 x 4096: 314 us against 361, 8192 x
+  // 4096 x 4096: 122 against 136, kNN 115 against 125; weight gradients, smaller beside their operands, gain 1% or lose
+  // 2%).  Pieces that are not whole lose by it: 1000 x 5003 in fp32, 25.8 us against 18.7.
+  const bool past = BM >= 128 && a.format != ZS_FORMAT_FP32 && ((uintptr_t)a.d | (uintptr_t)(a.ldd * 2)) % 64 == 0;
   float rs[FM];
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -584,7 +594,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
         v[r] = (float)sum[r] * rs[i];
         if (a.cs != nullptr) v[r] = v[r] * cs[r];
       }
-      if (m < a.M && n < a.N) store_run<kRun, (BM * BN > 64 * 64)>(a, m, n, v);
+      if (m < a.M && n < a.N) store_run<kRun>(a, m, n, v, past);
     }
   }
 }
@@ -1048,6 +1058,139 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_grad_tile(const Q8Gemm a, u
   }
 }
 
+// ---------------------------------------------------------------------------
+// Small weights, many tokens: 64 x 64 outputs per workgroup, whose eight waves
+// each take every eighth 32 tokens, with a part of LDS of their own that they
+// load three steps ahead and read through transposing reads: no wave waits for
+// another until their sums are added, in the waves' order.  The codes become
+// bf16 in the fragments: no other wave needs them.
+// ---------------------------------------------------------------------------
+template <bool TWO>
+__global__ __launch_bounds__(512, 2) void q8_grad_split(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {
+  constexpr int kWaves = 8, kRows = 32, kAhead = 3, kOps = 7;
+  constexpr int kAtX = kRows * 128, kAtS = kAtX + kRows * 64, kBuf = kAtS + 256;
+  constexpr int kPitch = 68;  // floats from row to row of the sums
+  constexpr int kLds = kWaves * kAhead * kBuf > kWaves * 64 * kPitch * 4 ? kWaves * kAhead * kBuf : kWaves * 64 * kPitch * 4;
+  __shared__ __attribute__((aligned(1024))) char lds[kLds];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, i16 = lane & 15;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * 64, n0 = (int64_t)tn * 64;
+  const int32_t T = (int32_t)a.K;
+  const int steps = (int)(((int64_t)T + kRows - 1) / kRows);
+  const int32_t wide_a = left_of(a.M, m0, 64) * 2, wide_b = left_of(a.N, n0, 64);
+  const int32_t pitch_a = (int32_t)a.lda * 2, pitch_b = (int32_t)a.ldb;
+  const uint32_t mine = (uint32_t)(uintptr_t)(LDS char*)lds + wave * kAhead * kBuf;
+  // piece c of row r at place c ^ s(r): the rows that 32 lanes read at a time in different banks
+  auto s_a = [](int r) { return (r >> 1 & 1) << 1 | (r >> 3 & 1) << 2; };
+  auto s_x = [](int r) { return (r >> 2 & 1) | (r >> 3 & 1) << 1; };
+  auto fetch = [&](int step, int buf) {
+    const int64_t t0 = (int64_t)step * kRows;
+    // the difference is right even where step * kRows passes 2^31
+    const int32_t left = (int32_t)((uint32_t)T - (uint32_t)step * (uint32_t)kRows), rows = max(min(left, kRows), 0);
+    const Rsrc ra = make_rsrc((const char*)a.a + (t0 * a.lda + m0) * 2, rows, wide_a, pitch_a);
+    const Rsrc rx = make_rsrc((const char*)a.b + t0 * a.ldb + n0, rows, wide_b, pitch_b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = j * 8 + (lane >> 3);
+      load_to_lds(ra, (uint32_t)(row * pitch_a + ((lane & 7) ^ s_a(row)) * 16), mine + buf * kBuf + j * 1024);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = j * 16 + (lane >> 2);
+      load_to_lds(rx, (uint32_t)(row * pitch_b + ((lane & 3) ^ s_x(row)) * 16), mine + buf * kBuf + kAtX + j * 1024);
+    }
+    load4_to_lds(make_rsrc(a.rs + t0, rows, 4, 4), (uint32_t)lane * 4, mine + buf * kBuf + kAtS);
+  };
+  f32x4 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+  for (int p = 0; p < kAhead; ++p) fetch(wave + p * kWaves, p);
+  int buf = 0;
+  for (int step = wave; step < steps; step += kWaves) {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kAhead - 1) * kOps) : "memory");
+    LDS char* p = (LDS char*)lds + (wave * kAhead + buf) * kBuf;
+    const f32x4 s0 = *(LDS f32x4*)(p + kAtS + g * 32), s1 = *(LDS f32x4*)(p + kAtS + g * 32 + 16);
+    i32x2 q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = 8 * g + (i16 >> 1);
+      q[j] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS i32x2*)(p + kAtX + row * 64 + (j ^ s_x(row)) * 16 + (i16 & 1) * 8));
+    }
+    bf16x8 fa[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 8 * g + (i16 >> 2);
+      LDS char* r = p + row * 128 + ((2 * i + (i16 >> 1 & 1)) ^ s_a(row)) * 16 + (i16 & 1) * 8;
+      const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)r);
+      const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(r + 4 * 128));
+      fa[i] = __builtin_bit_cast(bf16x8, (i16x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // all of the buffer is read
+    fetch(step + kAhead * kWaves, buf);
+    bf16x8 fb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u32x4 w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t c = (uint32_t)q[j][k / 2] >> (16 * (k % 2));
+        const f32x4& sc = k < 2 ? s0 : s1;
+        w[k] = pack_bf16((float)(int8_t)c * sc[k % 2 * 2], (float)(int8_t)(c >> 8) * sc[k % 2 * 2 + 1]);
+      }
+      fb[j] = __builtin_bit_cast(bf16x8, w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (TWO) {
+        u32x4 hi, lo;
+        fp16_parts(__builtin_bit_cast(u32x4, fa[i]), hi, lo);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], __builtin_bit_cast(bf16x8, hi), acc[i][j], 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], __builtin_bit_cast(bf16x8, lo), acc[i][j], 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+      }
+    }
+    buf = buf == kAhead - 1 ? 0 : buf + 1;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way to LDS
+  __syncthreads();
+  float* sums = (float*)lds;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *(f32x4*)(sums + (wave * 64 + i * 16 + i16) * kPitch + j * 16 + g * 4) = acc[i][j];
+  __syncthreads();
+  const int row = tid / 8, col = tid % 8 * 8;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int w = 0; w < kWaves; ++w) {
+    const f32x4 x = *(const f32x4*)(sums + (w * 64 + row) * kPitch + col);
+    const f32x4 y = *(const f32x4*)(sums + (w * 64 + row) * kPitch + col + 4);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = v[r] + x[r], v[4 + r] = v[4 + r] + y[r];
+  }
+  if (m0 + row < a.M && n0 + col < a.N) store_run<8>(a, m0 + row, n0 + col, v);
+}
+
+hipError_t grad_split_launch(const Q8Gemm& a, hipStream_t stream) {
+  const uint32_t tm = (uint32_t)((a.M + 63) / 64), tn = (uint32_t)((a.N + 63) / 64);
+  if (a.a_format == ZS_FORMAT_FP16)
+    q8_grad_split<true><<<dim3(tm * tn), 512, 0, stream>>>(a, tm, tn);
+  else
+    q8_grad_split<false><<<dim3(tm * tn), 512, 0, stream>>>(a, tm, tn);
+  return hipGetLastError();
+}
+
 template <DyPath PATH, int BM, int BN, int WM, int WN>
 hipError_t grad_tile_launch(const Q8Gemm& a, hipStream_t stream) {
   const uint32_t tm = (uint32_t)((a.M + BM - 1) / BM), tn = (uint32_t)((a.N + BN - 1) / BN);
@@ -1055,22 +1198,48 @@ hipError_t grad_tile_launch(const Q8Gemm& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// The weight gradient's kernel, by the time its grid needs for T tokens, in
+// stages of 64 (us, measured on 256 compute units at T = 1 to 16384; fp16, whose
+// stages are 32 tokens, takes about 1.8 times as long in each):
+//   64 x 64, tokens split over eight waves: 3.5 and 0.25 a stage for each 256
+//   128 x 128: 4.5 and 0.85 a stage up to 256 tiles, 1.12 for each 512
+//   256 x 256: 8 and 1.4 a stage up to 128 tiles, 1.85 for each 256
+// For example (T, N, K) = 8192, 1024, 1024: 33 / 111 / 171 us; 1025, 1376, 4096:
+// 42 / 24.5 / 31; 2000, 4096, 4096: 153 / 85 / 63; 100, 4096, 4096: 60 / 14.5 /
+// 13.1; 77, 1001, 517: 5.3 / 5.7 / 11.8.
+enum class GradTile { kSplit, k128, k256 };
+GradTile grad_tile_for(const Q8Gemm& a) {
+  const auto rounds = [](int64_t t, int64_t at_once) { return (double)((t + at_once - 1) / at_once); };
+  const int64_t t64 = tiles_of(a, 64, 64), t128 = tiles_of(a, 128, 128), t256 = tiles_of(a, 256, 256);
+  const double stages = (double)((a.K + 63) / 64);
+  const double split = (3.5 + 0.25 * stages) * rounds(t64, 256);
+  const double c128 = (4.5 + (t128 <= 256 ? 0.85 : 1.12) * stages) * rounds(t128, 512);
+  const double c256 = (8.0 + (t256 <= 128 ? 1.4 : 1.85) * stages) * rounds(t256, 256);
+  if (split <= c128 && split <= c256) return GradTile::kSplit;
+  return c128 <= c256 ? GradTile::k128 : GradTile::k256;
+}
+
 hipError_t grad_launch(const Q8Gemm& given, hipStream_t stream) {
   Q8Gemm a = given;
   const bool two = a.a_format == ZS_FORMAT_FP16;
-  const int64_t small = tiles_of(a, 128, 128), big = tiles_of(a, 256, 256);
-  if (small < 64 || small >= kMostTiles)
-    return two ? any_launch<Q8Op::kTN, kFP16>(a, stream) : any_launch<Q8Op::kTN, kBF16>(a, stream);
-  const bool aligned = rows16(a.a, a.K, a.lda * 2) && rows16(a.b, a.K, a.ldb);
-  if (aligned && a.K <= 1) a.lda = a.ldb = 256;  // a single row: any distance that holds what a tile reads of it
-  if (!aligned)
+  const int64_t tiles = tiles_of(a, 128, 128);
+  if (!rows16(a.a, a.K, a.lda * 2) || !rows16(a.b, a.K, a.ldb) || tiles_of(a, 64, 64) >= kMostTiles) {
+    // rows at any address: the kernel of 64 x 64 tiles spreads a small weight over more compute units
+    if (tiles < 64 || tiles >= kMostTiles)
+      return two ? any_launch<Q8Op::kTN, kFP16>(a, stream) : any_launch<Q8Op::kTN, kBF16>(a, stream);
     return two ? grad_tile_launch<DyPath::kPartsAny, 128, 128, 2, 2>(a, stream)
                : grad_tile_launch<DyPath::kThrough, 128, 128, 2, 2>(a, stream);
-  if (big >= 200)
-    return two ? grad_tile_launch<DyPath::kParts, 256, 256, 2, 4>(a, stream)
-               : grad_tile_launch<DyPath::kDirect, 256, 256, 2, 4>(a, stream);
-  return two ? grad_tile_launch<DyPath::kParts, 128, 128, 2, 2>(a, stream)
-             : grad_tile_launch<DyPath::kDirect, 128, 128, 2, 2>(a, stream);
+  }
+  if (a.K <= 1) a.lda = a.ldb = 256;  // a single row: any distance that holds what a tile reads of it
+  switch (grad_tile_for(a)) {
+    case GradTile::kSplit: return grad_split_launch(a, stream);
+    case GradTile::k128:
+      return two ? grad_tile_launch<DyPath::kParts, 128, 128, 2, 2>(a, stream)
+                 : grad_tile_launch<DyPath::kDirect, 128, 128, 2, 2>(a, stream);
+    default:
+      return two ? grad_tile_launch<DyPath::kParts, 256, 256, 2, 4>(a, stream)
+                 : grad_tile_launch<DyPath::kDirect, 256, 256, 2, 4>(a, stream);
+  }
 }
 
 }  // namespace
