@@ -66,10 +66,9 @@ __device__ __forceinline__ void fp16_parts(u32x4 h, u32x4& hi, u32x4& lo) {
 }
 
 // RUN (4 or 8) results at row m from column n on (those below N), plus what
-// add holds there; past: around the caches, where those are whole 64-byte
-// pieces.
-template <int FMT, int RUN>
-__device__ __forceinline__ void store_run_as(const Q8Gemm& a, int64_t m, int64_t n, float* v, bool past) {
+// add holds there.  PAST: around the caches, for 16-bit formats.
+template <int FMT, int RUN, bool PAST>
+__device__ __forceinline__ void store_run_as(const Q8Gemm& a, int64_t m, int64_t n, float* v) {
   const int64_t i = m * a.ldd + n;
   if (n + RUN <= a.N) {
     if (a.add != nullptr) {
@@ -92,7 +91,7 @@ __device__ __forceinline__ void store_run_as(const Q8Gemm& a, int64_t m, int64_t
     } else if constexpr (RUN == 8) {
       const u32x4 w = {pack_two<FMT>(v[0], v[1]), pack_two<FMT>(v[2], v[3]), pack_two<FMT>(v[4], v[5]),
                        pack_two<FMT>(v[6], v[7])};
-      if (past)
+      if constexpr (PAST)
         st_past((uint16_t*)a.d + i, w);
       else
         st_any((uint16_t*)a.d + i, w);
@@ -106,14 +105,14 @@ __device__ __forceinline__ void store_run_as(const Q8Gemm& a, int64_t m, int64_t
     }
   }
 }
-template <int RUN>
-__device__ __forceinline__ void store_run(const Q8Gemm& a, int64_t m, int64_t n, float* v, bool past = false) {
+template <int RUN, bool PAST = false>
+__device__ __forceinline__ void store_run(const Q8Gemm& a, int64_t m, int64_t n, float* v) {
   if (a.format == ZS_FORMAT_BF16)
-    store_run_as<kBF16, RUN>(a, m, n, v, past);
+    store_run_as<kBF16, RUN, PAST>(a, m, n, v);
   else if (a.format == ZS_FORMAT_FP16)
-    store_run_as<kFP16, RUN>(a, m, n, v, past);
+    store_run_as<kFP16, RUN, PAST>(a, m, n, v);
   else
-    store_run_as<kFP32, RUN>(a, m, n, v, past);
+    store_run_as<kFP32, RUN, PAST>(a, m, n, v);
 }
 
 // Two accumulators side by side (columns 4 g + r of one 16-column fragment and
@@ -388,7 +387,7 @@ __device__ __forceinline__ int place_nn(int r) {
   return BN > 64 ? r & 7 : (r >> 2 & 1) | (r >> 4 & 1) << 1;
 }
 
-template <Q8Op OP, int BM, int BN, int WM, int WN, int NS>
+template <Q8Op OP, int BM, int BN, int WM, int WN, int NS, bool PAST>
 __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {
   constexpr bool kNT = OP == Q8Op::kNT;
   constexpr int kWaves = WM * WN;
@@ -554,10 +553,6 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
   // so that a store covers 64 bytes of each of 16 rows (with 4 columns a lane, kNN took 4-20% longer: 148 us against 120
   // at 8192 x 4096 x 4096).
   constexpr int kRun = 8;
-  // Large 16-bit outputs otherwise push the operands out of the caches (8192 x 11008 x 4096: 314 us against 361, 8192 x
-  // 4096 x 4096: 122 against 136, kNN 115 against 125; weight gradients, smaller beside their operands, gain 1% or lose
-  // 2%).  Pieces that are not whole lose by it: 1000 x 5003 in fp32, 25.8 us against 18.7.
-  const bool past = BM >= 128 && a.format != ZS_FORMAT_FP32 && ((uintptr_t)a.d | (uintptr_t)(a.ldd * 2)) % 64 == 0;
   float rs[FM];
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -594,7 +589,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
         v[r] = (float)sum[r] * rs[i];
         if (a.cs != nullptr) v[r] = v[r] * cs[r];
       }
-      if (m < a.M && n < a.N) store_run<kRun>(a, m, n, v, past);
+      if (m < a.M && n < a.N) store_run<kRun, PAST>(a, m, n, v);
     }
   }
 }
@@ -758,8 +753,17 @@ hipError_t split_launch(const Q8Gemm& a, hipStream_t stream) {
 
 template <Q8Op OP, int BM, int BN, int WM, int WN, int NS>
 hipError_t tile_launch(const Q8Gemm& a, hipStream_t stream) {
-  const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
-  q8_gemm_tile<OP, BM, BN, WM, WN, NS><<<dim3((unsigned)(tm * tn)), WM * WN * 64, 0, stream>>>(a, (uint32_t)tm, (uint32_t)tn);
+  const uint32_t tm = (uint32_t)((a.M + BM - 1) / BM), tn = (uint32_t)((a.N + BN - 1) / BN);
+  // Large 16-bit outputs otherwise push the operands out of the caches (8192 x 11008 x 4096: 314 us against 361, 8192 x
+  // 4096 x 4096: 122 against 136, kNN 115 against 125; weight gradients, smaller beside their operands, gain 1% or lose
+  // 2%).  Pieces that are not whole 64 bytes lose by it: 1000 x 5003 in fp32, 25.8 us against 18.7.
+  if constexpr (BM >= 128) {
+    if (a.format != ZS_FORMAT_FP32 && ((uintptr_t)a.d | (uintptr_t)(a.ldd * 2)) % 64 == 0) {
+      q8_gemm_tile<OP, BM, BN, WM, WN, NS, true><<<dim3(tm * tn), WM * WN * 64, 0, stream>>>(a, tm, tn);
+      return hipGetLastError();
+    }
+  }
+  q8_gemm_tile<OP, BM, BN, WM, WN, NS, false><<<dim3(tm * tn), WM * WN * 64, 0, stream>>>(a, tm, tn);
   return hipGetLastError();
 }
 

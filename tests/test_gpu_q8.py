@@ -195,20 +195,23 @@ def test_matmul(zs, T, N, K, trans_w):
         assert by.untouched_outside()
 
 
-# enough output for the widest tiles, with edges inside them on both sides and at the end of the summed axis
-WIDE = [(4100, 3300, 272), (3333, 4097, 200), (2100, 8200, 1000)]
+# enough output for the wider tiles, with edges inside them on both sides and at the end of the summed axis; rows on
+# 16-byte boundaries, then anywhere
+WIDE = [(4100, 3300, 272), (3333, 4097, 200), (2100, 8200, 1000), (1500, 1530, 200)]
 
 
+@pytest.mark.parametrize("aligned", [True, False])
 @pytest.mark.parametrize("trans_w", [True, False])
 @pytest.mark.parametrize("rows,cols,inner", WIDE)
-def test_matmul_wide(zs, rows, cols, inner, trans_w):
+def test_matmul_wide(zs, rows, cols, inner, trans_w, aligned):
     rng = np.random.default_rng(rows)
     N, K = (cols, inner) if trans_w else (inner, cols)
     x, w = random_codes(rng, rows, inner), random_codes(rng, N, K)
     sx, sw = random_scales(rng, rows, pow2=False), random_scales(rng, cols, pow2=False)
-    bx, bw = Buf(rows, inner, torch.int8, -inner % 16, 0, x), Buf(N, K, torch.int8, -K % 16, 16, w)
-    for kind in ("bf16", "fp32"):
-        by = Buf(rows, cols, DT[kind], 3, 1)
+    gaps = (-inner % 16, -K % 16, 16) if aligned else (5, 3, 1)
+    bx, bw = Buf(rows, inner, torch.int8, gaps[0], 0, x), Buf(N, K, torch.int8, gaps[1], gaps[2], w)
+    for kind, gap_y, lead_y in (("bf16", -cols % 32, 0), ("bf16", 3, 1), ("fp16", -cols % 32, 32), ("fp32", 3, 1)):
+        by = Buf(rows, cols, DT[kind], gap_y, lead_y)
         zs.q8_matmul(bx.t, sx.cuda(), bw.t, sw.cuda(), by.t, trans_w=trans_w)
         y = ref.product(x.cuda(), sx.cuda(), w.cuda(), sw.cuda(), trans_w).cpu()
         bad = ref.outside(by.t, y, ref.product_tolerance(y, kind), kind)
@@ -216,13 +219,15 @@ def test_matmul_wide(zs, rows, cols, inner, trans_w):
         assert by.untouched_outside()
 
 
+@pytest.mark.parametrize("aligned", [True, False])
 @pytest.mark.parametrize("dy_kind", ["bf16", "fp16"])
-@pytest.mark.parametrize("rows,cols,inner", WIDE)
-def test_weight_grad_wide(zs, rows, cols, inner, dy_kind):
+@pytest.mark.parametrize("rows,cols,inner", WIDE + [(100, 130, 5000), (64, 65, 4097), (700, 640, 3001)])
+def test_weight_grad_wide(zs, rows, cols, inner, dy_kind, aligned):
     rng = np.random.default_rng(cols)
     dy = activations(rng, inner, rows).mul(1e-2).to(DT[dy_kind])
     x, sx = random_codes(rng, inner, cols), random_scales(rng, inner)
-    bdy, bx = Buf(inner, rows, DT[dy_kind], -rows % 8, 0, dy), Buf(inner, cols, torch.int8, -cols % 16, 16, x)
+    gaps = (-rows % 8, -cols % 16, 16) if aligned else (3, 5, 1)
+    bdy, bx = Buf(inner, rows, DT[dy_kind], gaps[0], 0, dy), Buf(inner, cols, torch.int8, gaps[1], gaps[2], x)
     dy, x, sx = dy.cuda(), x.cuda(), sx.cuda()
     for kind in (dy_kind, "fp32"):
         b = activations(rng, rows, cols).to(DT[kind])
@@ -233,6 +238,17 @@ def test_weight_grad_wide(zs, rows, cols, inner, dy_kind):
         bad = ref.outside(bw.t, want, tolerance, kind)
         assert not bad.any(), f"{kind}: {int(bad.sum())} of {bad.numel()} off"
         assert bw.untouched_outside()
+
+
+@pytest.mark.parametrize("T,N", [(1, 5), (20, 300), (700, 700)])
+def test_matmul_over_nothing(zs, T, N):
+    y = torch.ones(T, N, device="cuda")
+    x, w, s = (torch.empty(T, 0, dtype=torch.int8, device="cuda"), torch.empty(N, 0, dtype=torch.int8, device="cuda"),
+               torch.ones(T, device="cuda"))
+    zs.q8_matmul(x, s, w, None, y)
+    assert not y.any()
+    zs.q8_matmul(x, s, torch.empty(0, N, dtype=torch.int8, device="cuda"), None, y.fill_(1), trans_w=False)
+    assert not y.any()
 
 
 def test_matmul_sums_are_exact_at_the_longest_axis(zs):
