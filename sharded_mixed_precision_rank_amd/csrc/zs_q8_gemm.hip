@@ -131,7 +131,7 @@ __device__ __forceinline__ void trade(uint32_t x, uint32_t y, uint32_t& lo, uint
 // operands staged through registers 16 bytes at a time, so that rows may start
 // at any address and end anywhere.  The first operand of the matrix
 // instruction is b's, so that a lane ends with four consecutive columns of a
-// row.
+// row.  8192 x 11008 x 4096: 794 us, kNN 1392, kTN 2079.
 // ---------------------------------------------------------------------------
 constexpr int kAnyTile = 64;
 constexpr int kAnyK = 128;   // codes along K per step (kNT, kNN)
@@ -287,11 +287,20 @@ hipError_t any_launch(const Q8Gemm& a, hipStream_t stream) {
 // ---------------------------------------------------------------------------
 // Code rows on 16-byte boundaries: BM x BN outputs per workgroup of WM x WN
 // waves, pieces of both operands moved from memory into LDS directly, 128
-// codes of K a stage and two stages.  A wave holds its fragments of the next 64
-// codes in registers while the matrix instructions take the current ones, so
-// LDS reads, memory loads and matrix instructions run side by side with one
-// or two waves per SIMD.  One barrier a stage: between its halves every wave has read
-// all of the stage and its part of the next one has arrived.
+// codes of the summed axis a stage and NS stages in a ring.  A wave holds its
+// fragments of the next 64 codes in registers while the matrix instructions
+// take the current ones, so that LDS reads, memory loads and matrix
+// instructions run side by side.  One barrier a stage: between its halves every
+// wave has read all of the stage and its part of the next one has landed.
+//
+// 256 x 256 by eight waves (128 x 64 each, 245 registers, 128 KB of LDS):
+// 8192 x 11008 x 4096 in 314-330 us (2240-2350 TOP/s), its input gradient in 282-287
+// (2580-2620), where a library's int8 product takes 357 (2071).  Of 119 us at
+// 8192 x 4096 x 4096, the matrix instructions alone take 79 (the clock falls
+// under them, to about 1.7 GHz) and the loads alone 102.  Four waves of 128 x
+// 128 spill or shuffle accumulators (309-909 us); stages of 64 codes in a ring of
+// four or five load half lines and are slower (125 against 119, kNN 156 against
+// 125).  Bank conflicts: none, by counter.
 // ---------------------------------------------------------------------------
 typedef uint32_t Rsrc __attribute__((ext_vector_type(4)));
 
@@ -344,7 +353,8 @@ __device__ __forceinline__ float ld_buffer4(Rsrc r, uint32_t voff) {
 
 // The tile of workgroup `bid`: workgroups go to the eight XCDs in turn, so
 // each XCD takes a run of consecutive tiles, which go down groups of 8 tile
-// rows: its L2 sees few rows and columns of operands at a time.
+// rows: its L2 sees few rows and columns of operands at a time (groups of 4 or
+// 16: the same or up to 5% slower).
 __device__ __forceinline__ void tile_of(uint32_t bid, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
   const uint32_t total = tiles_m * tiles_n;
   const uint32_t x = bid % 8, per = total / 8, more = total % 8;
@@ -601,7 +611,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
 // another's operands: kNT reads fragments from memory straight into
 // registers; kNN moves them through a part of LDS of the wave's own, to turn
 // the weight's rows.  The waves' sums meet in LDS (integer additions, whose
-// order does not matter).
+// order does not matter).  Bound by the weight's bytes: one token, N = 4096: K =
+// 4096 in 6.2 us, 11008 in 10.9 (4.1 TB/s).
 // ---------------------------------------------------------------------------
 template <Q8Op OP, int MT, int NT, int W>
 __global__ __launch_bounds__(W * 64, 2) void q8_gemm_split(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {
@@ -834,6 +845,14 @@ hipError_t product_launch(const Q8Gemm& given, hipStream_t stream) {
 // bf16 parts of 32 tokens a stage when it is fp16 (kParts, kPartsAny), or as it
 // is (kThrough).  kDirect and kParts want rows on 16-byte boundaries, the others
 // take any.
+//
+// kDirect, 256 x 256: T, N, K = 8192, 11008, 4096 in 600-640 us (1150-1230
+// TFLOP/s; a library's bf16 product of the same layout 797), 8192, 4096, 4096 in
+// 236.  Of those 236, the matrix instructions take 136 and with the fragments'
+// reads 181; the codes' fetch adds 30, dy's loads 17, the conversion 8: a fetch
+// waits on memory for more than the stage that it has.  Slower: 32-token stages
+// in a ring of four with the codes loaded to LDS as they are (256); the waves in
+// two groups half a stage apart (311); the codes fetched after dy's loads (284).
 // ---------------------------------------------------------------------------
 enum class DyPath { kDirect, kParts, kThrough, kPartsAny };
 
@@ -1067,7 +1086,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_grad_tile(const Q8Gemm a, u
 // each take every eighth 32 tokens, with a part of LDS of their own that they
 // load three steps ahead and read through transposing reads: no wave waits for
 // another until their sums are added, in the waves' order.  The codes become
-// bf16 in the fragments: no other wave needs them.
+// bf16 in the fragments: no other wave needs them.  T, N, K = 8192, 256, 256: 28
+// us (in 128 x 128 tiles 105), bound by the loads' latency.
 // ---------------------------------------------------------------------------
 template <bool TWO>
 __global__ __launch_bounds__(512, 2) void q8_grad_split(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {

@@ -259,13 +259,30 @@ def test_matmul_sums_are_exact_at_the_longest_axis(zs):
     x[2, ::2] = 127
     w = torch.full((20, K), -128, dtype=torch.int8)
     w[7] = 127
-    one = torch.ones(3)
+    want = (x.double() @ w.double().t()).float()  # f32 of the exact sum
+    for rows in (3, 100):  # by the few-row kernels, and in tiles
+        xr = x[torch.arange(rows) % 3]
+        for pad in (0, 1):  # rows anywhere, and on 16-byte boundaries
+            for trans_w in (True, False):
+                wt = w if trans_w else w.t().contiguous()
+                bx = Buf(rows, K, torch.int8, pad, 0, xr)
+                bw = Buf(*wt.shape, torch.int8, -wt.shape[1] % 16 if pad else 0, 0, wt)
+                y = torch.empty(rows, 20, device="cuda")
+                zs.q8_matmul(bx.t, torch.ones(rows, device="cuda"), bw.t, None, y, trans_w=trans_w)
+                assert torch.equal(y.cpu(), want[torch.arange(rows) % 3]), (rows, pad, trans_w)
+
+
+def test_matmul_of_many_columns(zs):
+    """More outputs than a product may sum over: only the summed axis has that limit."""
+    rng = np.random.default_rng(14)
+    x, w = random_codes(rng, 3, 48), random_codes(rng, 140001, 48)
+    s = random_scales(rng, 3)
     for trans_w in (True, False):
         wt = w if trans_w else w.t().contiguous()
-        y = torch.empty(3, 20, device="cuda")
-        zs.q8_matmul(x.cuda(), one.cuda(), wt.cuda(), None, y, trans_w=trans_w)
-        want = (x.double() @ w.double().t()).float()  # f32 of the exact sum
-        assert torch.equal(y.cpu(), want)
+        y = torch.empty(3, 140001, device="cuda")
+        zs.q8_matmul(x.cuda(), s.cuda(), wt.cuda(), None, y, trans_w=trans_w)
+        want = ref.product(x, s, wt, None, trans_w)
+        assert not ref.outside(y, want, ref.product_tolerance(want, "fp32"), "fp32").any()
 
 
 def test_matmul_nan_scale_marks_its_row_only(zs):
