@@ -819,13 +819,14 @@ hipError_t product_launch(const Q8Gemm& given, hipStream_t stream) {
   // a single row: any distance that holds what a tile reads of it
   if (a.M <= 1) a.lda = (a.K + 15) / 16 * 16;
   if (rows_b <= 1) a.ldb = OP == Q8Op::kNT ? (a.K + 15) / 16 * 16 : 256;
-  // Few rows: their tiles of 64 columns may be too few to draw on all of the memory.  One token, K = 4096: 6.2 us
+  // Few rows: their tiles of 64 columns may be too few to draw on all of the memory.  kNT, K = 4096: one token 6.2 us
   // against 9.2 in 64 x 64 tiles for N = 4096, 11.8 against 10.0 for N = 11008; 16 tokens 7.8 / 9.4 and 16.3 / 9.8.
-  // kNN: 10.6 / 11.5 with N = K = 4096, 10.7 / 11.9 with N = 4096 rows of K = 11008.
+  // kNN, tiles of 16 x 64: 61 tokens 10.1 / 13.4 for 4096 columns (256 tiles), 21.0 / 14.2 for 11008 (688); 16 tokens
+  // 11.2 / 12.3 for 11008 (172), 32 tokens 17.1 / 12.7 (344).
   if constexpr (OP == Q8Op::kNT) {
     if (a.M <= 16 && (a.N + 63) / 64 <= 96) return split_launch<OP, 1, 1, 4>(a, stream);
   } else {
-    if (a.M <= 16) return split_launch<OP, 1, 4, 8>(a, stream);
+    if (tiles_of(a, 16, 64) <= 256) return split_launch<OP, 1, 4, 8>(a, stream);
   }
   switch (tile_for(a)) {
     case Tile::k64: return tile_launch<OP, 64, 64, 4, 1, 4>(a, stream);
