@@ -794,17 +794,20 @@ constexpr int64_t kMostTiles = 1 << 22;
 //     tiles, 1.7-1.9 a round where there are more;
 //   128 x 128: 0.45-0.7 up to 256 tiles with four stages, beyond that two
 //     workgroups of two stages a unit, 0.8-1.15 for each 512;
+//   96 x 64: 0.36-0.40 up to 256 tiles; beyond that one of the others is as
+//     good or better (640 x 4096: 19.5 us, 128 x 128 18.2);
 //   64 x 64: 0.25-0.33 up to 256 tiles, 0.45-0.5 for each 512.
 // For example 8192 x 11008 by 4096: 346 / 407 / 616 us; 2000 x 4096: 44.7 /
 // 36.2 / 59.5; 1000 x 4096: 42.4 / 21.8 / 31.2; 333 x 4096: 41.5 / 16.5 /
-// 15.2; 61 x 11008: 38.6 / 16.2 / 10.7.
-enum class Tile { k64, k128, k128Far, k256 };
+// 15.2, in 96 x 64 13.6 (K = 11008: 37.4, in 96 x 64 31.4); 61 x 11008: 38.6 / 16.2 / 10.7.
+enum class Tile { k64, k96, k128, k128Far, k256 };
 Tile tile_for(const Q8Gemm& a) {
   const auto rounds = [](int64_t t, int64_t at_once) { return (double)((t + at_once - 1) / at_once); };
-  const int64_t t64 = tiles_of(a, 64, 64), t128 = tiles_of(a, 128, 128), t256 = tiles_of(a, 256, 256);
+  const int64_t t64 = tiles_of(a, 64, 64), t96 = tiles_of(a, 96, 64), t128 = tiles_of(a, 128, 128), t256 = tiles_of(a, 256, 256);
   const double c64 = t64 <= 256 ? 0.30 : 0.475 * rounds(t64, 512);
   const double c128 = t128 <= 256 ? 0.50 + 0.18 * (double)t128 / 256 : t128 <= 512 ? 0.65 + 0.45 * (double)t128 / 512 : 1.1 * rounds(t128, 512);
   const double c256 = t256 <= 256 ? 1.40 : 1.8 * rounds(t256, 256);
+  if (t64 > 256 && t96 <= 256) return Tile::k96;
   if (c64 <= c128 && c64 <= c256) return Tile::k64;
   if (c128 <= c256) return t128 <= 256 ? Tile::k128Far : Tile::k128;
   return Tile::k256;
@@ -830,6 +833,7 @@ hipError_t product_launch(const Q8Gemm& given, hipStream_t stream) {
   }
   switch (tile_for(a)) {
     case Tile::k64: return tile_launch<OP, 64, 64, 4, 1, 4>(a, stream);
+    case Tile::k96: return tile_launch<OP, 96, 64, 2, 2, 4>(a, stream);
     case Tile::k128Far: return tile_launch<OP, 128, 128, 4, 2, 4>(a, stream);
     case Tile::k128: return tile_launch<OP, 128, 128, 2, 2, 2>(a, stream);
     default: return tile_launch<OP, 256, 256, 2, 4, 2>(a, stream);

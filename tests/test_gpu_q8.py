@@ -198,11 +198,13 @@ def test_matmul(zs, T, N, K, trans_w):
 # enough output for the wider tiles, with edges inside them on both sides and at the end of the summed axis; rows on
 # 16-byte boundaries, then anywhere
 WIDE = [(4100, 3300, 272), (3333, 4097, 200), (2100, 8200, 1000), (1500, 1530, 200)]
+# the smaller tiles, where there are enough of them that the summed axis is not split (input gradients too)
+FEW_ROWS = [(370, 3001, 1000), (140, 6001, 333), (100, 10001, 200), (60, 17000, 1111)]
 
 
 @pytest.mark.parametrize("aligned", [True, False])
 @pytest.mark.parametrize("trans_w", [True, False])
-@pytest.mark.parametrize("rows,cols,inner", WIDE)
+@pytest.mark.parametrize("rows,cols,inner", WIDE + FEW_ROWS)
 def test_matmul_wide(zs, rows, cols, inner, trans_w, aligned):
     rng = np.random.default_rng(rows)
     N, K = (cols, inner) if trans_w else (inner, cols)
