@@ -817,7 +817,8 @@ template <Q8Op OP>
 hipError_t product_launch(const Q8Gemm& given, hipStream_t stream) {
   Q8Gemm a = given;
   const int64_t rows_b = OP == Q8Op::kNT ? a.N : a.K;
-  if (!rows16(a.a, a.M, a.lda) || !rows16(a.b, rows_b, a.ldb) || tiles_of(a, 64, 64) >= kMostTiles)
+  // (an empty sum goes there too: its operands may be NULL, and q8_gemm_split fetches before it looks at the length)
+  if (a.K == 0 || !rows16(a.a, a.M, a.lda) || !rows16(a.b, rows_b, a.ldb) || tiles_of(a, 64, 64) >= kMostTiles)
     return any_launch<OP, kBF16>(a, stream);
   // a single row: any distance that holds what a tile reads of it
   if (a.M <= 1) a.lda = (a.K + 15) / 16 * 16;

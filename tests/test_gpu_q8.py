@@ -242,6 +242,21 @@ def test_weight_grad_wide(zs, rows, cols, inner, dy_kind, aligned):
         assert bw.untouched_outside()
 
 
+@pytest.mark.parametrize("T,N", [(1, 64), (2, 64), (16, 300), (100, 500), (700, 900)])
+def test_matmul_of_empty_slices(zs, T, N):
+    """Operands without columns whose rows lie 16 bytes apart: torch gives their address as NULL."""
+    x, w, s = (torch.ones(T, 16, dtype=torch.int8, device="cuda")[:, :0], torch.ones(N, 16, dtype=torch.int8, device="cuda")[:, :0],
+               torch.ones(T, device="cuda"))
+    assert x.stride() == (16, 1) and w.stride() == (16, 1)
+    y = torch.ones(T, N, device="cuda")
+    zs.q8_matmul(x, s, w, torch.ones(N, device="cuda"), y)
+    assert (y.cpu() == 0).all()
+    y = torch.ones(T, N, device="cuda")
+    wide = torch.ones(16, N, dtype=torch.int8, device="cuda")[:0]
+    zs.q8_matmul(x, s, wide, None, y, trans_w=False)
+    assert (y.cpu() == 0).all()
+
+
 @pytest.mark.parametrize("T,N", [(1, 5), (20, 300), (700, 700)])
 def test_matmul_over_nothing(zs, T, N):
     y = torch.ones(T, N, device="cuda")
