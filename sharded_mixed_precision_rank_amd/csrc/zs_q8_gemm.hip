@@ -323,20 +323,16 @@ __device__ __forceinline__ int32_t left_of(int64_t total, int64_t done, int32_t 
 
 // 64 lanes' 16 bytes each, from rsrc + voff, to LDS at lds + 16 * lane.  The
 // whole offset is in voff: the bounds check is against that.  The caller waits
-// (vmcnt) before anyone reads them, and before the workgroup ends.
+// (vmcnt) before anyone reads them, and before the workgroup ends.  The LDS
+// address is an operand in m0, so that the compiler knows of every write to
+// that register; a load that follows the write needs one wait state.
 __device__ __forceinline__ void load_to_lds(Rsrc rsrc, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-               :
-               : "v"(voff), "s"(rsrc), "s"(lds)
-               : "memory");
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(voff), "s"(rsrc), "{m0}"(lds) : "memory");
 }
 
 // The same with 4 bytes a lane.
 __device__ __forceinline__ void load4_to_lds(Rsrc rsrc, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds"
-               :
-               : "v"(voff), "s"(rsrc), "s"(lds)
-               : "memory");
+  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" : : "v"(voff), "s"(rsrc), "{m0}"(lds) : "memory");
 }
 
 // Sixteen bytes of a buffer (zeros past its end).
