@@ -426,11 +426,14 @@ ZS_API zs_status zs_cpu_adam(const float* gbar, int64_t n, float* master, float*
  * rows in elements (at least the columns; not looked at for a single row).
  * Any alignment of the elements works; code rows that start on 16-byte
  * boundaries (base and ld), and dy rows that do, run fastest.  Dimensions are
- * 0 .. 2^31 - 1.  An output may share no byte with an input or another output
- * (column ranges of one buffer, with one ld, may interleave).  Nothing but the
- * outputs' own rows and columns is written.  No workspace, no allocation;
- * every call enqueues kernels on `stream` only and may be captured.  Results
- * do not depend on what runs beside them, call to call.
+ * 0 .. 2^31 - 1.  An output may share no byte with an input or another output:
+ * column ranges of one buffer, with one distance in bytes between their rows,
+ * may interleave, and a vector or a single row may lie between the rows of a
+ * matrix; matrices of several rows at different distances are refused where
+ * their ranges meet.  Nothing but the outputs' own rows and columns is written.
+ * No workspace, no allocation; every call enqueues kernels on `stream` only and
+ * may be captured.  Results do not depend on what runs beside them, call to
+ * call.
  *
  * Non-finite values: a row that holds a NaN or an infinity gets the scale NaN
  * and codes 0, so that everything made from it is NaN and a loss scaler that

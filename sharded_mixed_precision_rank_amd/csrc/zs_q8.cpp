@@ -31,13 +31,19 @@ Region vector_of(const char* name, const void* p, int64_t n) {
 }
 
 // Whether two matrices share a byte.  Column ranges of one buffer (the same
-// pitch) may interleave without sharing any.
+// pitch) may interleave without sharing any, and a single row (a vector too)
+// may lie in a gap between a matrix's rows.  Matrices of several rows at
+// different pitches count as sharing one where their ranges meet.
 bool overlap(const Region& a, const Region& b) {
   if (a.empty() || b.empty() || a.end() <= b.base || b.end() <= a.base) return false;
-  if (a.pitch != b.pitch || a.rows == 1 || b.rows == 1) return true;
-  const uintptr_t p = (uintptr_t)a.pitch;
-  const int64_t d = (int64_t)(a.base < b.base ? (b.base - a.base) % p : (p - (a.base - b.base) % p) % p);
-  return !(d >= a.width && d + b.width <= a.pitch);
+  if (a.rows == 1 && b.rows == 1) return true;
+  if (a.rows > 1 && b.rows > 1 && a.pitch != b.pitch) return true;
+  const Region &many = a.rows > 1 ? a : b, &other = a.rows > 1 ? b : a;
+  const uintptr_t p = (uintptr_t)many.pitch;
+  // where the other begins in the rows' period: behind a row's bytes, with its own ending before the next?
+  const int64_t d = (int64_t)(many.base < other.base ? (other.base - many.base) % p
+                                                     : (p - (many.base - other.base) % p) % p);
+  return !(d >= many.width && d + other.width <= many.pitch);
 }
 
 zs_status check_dim(const char* name, int64_t n) {

@@ -1,7 +1,13 @@
 """The 8-bit training operators on the CPU: what their sources, header and argument checks promise."""
 import os
+import random
 import re
 
+import sharded_mixed_precision_rank_amd as zs
+
+LIB = zs.library()
+A = 0x7F0000000000  # never dereferenced: every call here fails before any HIP call
+MB = 1 << 20
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "sharded_mixed_precision_rank_amd", "csrc")
 
@@ -37,3 +43,57 @@ def test_loads_to_lds_take_m0_as_an_operand():
                 assert '"{m0}"' in text, (name, instruction)
                 found += 1
     assert found == 2
+
+
+def _shared(a, b):
+    """Whether two matrices (base, rows, bytes a row, pitch) share a byte, by their bytes."""
+    bytes_of = lambda base, rows, width, pitch: {base + r * pitch + k for r in range(rows) for k in range(width)}  # noqa: E731
+    return bool(bytes_of(*a) & bytes_of(*b))
+
+
+def test_a_single_row_may_lie_between_the_rows_of_a_matrix():
+    """An output is refused where it shares a byte with an input, not where it lies in a gap between its rows.  One
+    token's product y beside the weight's rows; w_scales is y itself, so that every call is refused before it launches
+    anything, and the message says for which of the two."""
+    rng = random.Random(1)
+    met = {False: 0, True: 0}
+    for _ in range(4000):
+        n, k = rng.randint(1, 6), rng.randint(1, 12)
+        ld = k + rng.choice((0, 1, rng.randint(1, 40)))
+        at = A + rng.randint(-40, n * ld + 8) // 4 * 4
+        status = LIB.zs_q8_matmul(A + MB, k, A + 2 * MB, A, ld, at, 1, n, k, 0, at, 0, n, None)
+        message = LIB.zs_last_error().decode()
+        want = _shared((at, 1, 2 * n, 2 * n), (A, n, k, ld))
+        assert zs.STATUS[status] == "ZS_ERR_ALIAS", message
+        assert ("overlaps w_codes" in message) == want, (n, k, ld, at - A, message)
+        assert want or "overlaps w_scales" in message
+        met[want] += 1
+    assert min(met.values()) > 300
+
+
+def test_a_vector_may_lie_between_the_rows_of_a_matrix():
+    """The scales somewhere about x's rows; the column factors are the scales themselves, which is refused last."""
+    rng = random.Random(2)
+    met = {False: 0, True: 0}
+    for _ in range(4000):
+        rows, cols = rng.randint(2, 6), rng.randint(1, 12)
+        ld = cols + rng.choice((0, 1, rng.randint(1, 40)))
+        at = A + rng.randint(-40, rows * ld * 2 + 8) // 4 * 4
+        status = LIB.zs_q8_save(A, 0, ld, rows, cols, at, 0, A + MB, cols, at, None)
+        message = LIB.zs_last_error().decode()
+        want = _shared((at, 1, 4 * rows, 4 * rows), (A, rows, 2 * cols, 2 * ld))
+        assert zs.STATUS[status] == "ZS_ERR_ALIAS", message
+        assert ("scales overlaps x" in message) == want, (rows, cols, ld, at - A, message)
+        assert want or "scales overlaps col_scale" in message
+        met[want] += 1
+    assert min(met.values()) > 300
+
+
+def test_rows_at_different_distances_are_refused_where_their_ranges_meet():
+    """Two matrices of several rows: told apart where their rows lie at the same distance, refused otherwise."""
+    codes = dict(x=A + 64, T=4, K=16)
+    for ld_y, want in ((32, "ZS_ERR_ALIAS"), (64, "ZS_ERR_ALIAS")):
+        status = LIB.zs_q8_matmul(codes["x"], 128, A + MB, A + 2 * MB, 16, A, 4, 8, 16, 0, A, 0, ld_y, None)
+        message = LIB.zs_last_error().decode()
+        assert zs.STATUS[status] == want
+        assert ("overlaps x_codes" in message) == (ld_y != 64), message
