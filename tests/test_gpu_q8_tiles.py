@@ -1,0 +1,158 @@
+"""The tiled kernels of the 8-bit weight gradient (128 x 128 and 256 x 256, operands loaded to LDS directly or through
+registers) and the split one, at scales that are no power of two, non-finite values, long sums that have to be exact,
+captured graphs and repeated calls.  Plain forms in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+from tests import q8_ref as ref
+from tests.test_gpu_q8 import Buf, _layer, _layer_buffers, activations, random_codes, random_scales, same_bits
+
+pytestmark = pytest.mark.gpu
+
+DT = ref.DT
+# (T, N, K): few weights, split over tokens; 12 x 12 tiles of 128; 17 x 13 tiles of 256 (rows anywhere: 128 x 128)
+SHAPES = [(300, 130, 200), (200, 1500, 1530), (272, 4100, 3300)]
+
+
+@pytest.fixture(scope="module")
+def zs():
+    import sharded_mixed_precision_rank_amd as zs
+
+    return zs
+
+
+def operands(dy, x, aligned):
+    """Views of dy and x with rows on 16-byte boundaries, or anywhere."""
+    (T, N), K = dy.shape, x.shape[1]
+    gaps = (-N % 8, -K % 16, 16) if aligned else (3, 5, 1)
+    return Buf(T, N, dy.dtype, gaps[0], 0 if aligned else 1, dy).t, Buf(T, K, torch.int8, gaps[1], gaps[2], x).t
+
+
+def rounded_operand(x, sx):
+    """A code times its scale as the contract has it: the fp32 product rounded to bf16."""
+    return (x.to(torch.float32) * sx[:, None]).to(torch.bfloat16).double()
+
+
+def gradient(dy, x, sx):
+    """dw in 64 bits from the rounded operand, and the error of its fp32 sums: T additions (twice that for fp16's two
+    parts), each off by at most one step, 2^-23, of the partial sums' bound."""
+    w = rounded_operand(x, sx)
+    dw = dy.double().t() @ w
+    n = dy.shape[0] * (2 if dy.dtype == torch.float16 else 1) + 2
+    return dw, (dy.double().abs().t() @ w.abs()) * n * 2.0 ** -23
+
+
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,N,K", SHAPES)
+def test_scales_that_are_no_power_of_two(zs, T, N, K, kind, aligned):
+    rng = np.random.default_rng(T + N)
+    dy = activations(rng, T, N).mul(1e-2).to(DT[kind]).cuda()
+    x, sx = random_codes(rng, T, K).cuda(), random_scales(rng, T, pow2=False).cuda()
+    bdy, bx = operands(dy, x, aligned)
+    dw = torch.empty(N, K, device="cuda")
+    zs.q8_weight_grad(bdy, bx, sx, dw)
+    want, slack = gradient(dy, x, sx)
+    slack = slack + (want.abs() + slack) * ref.U32
+    off = (dw.double() - want).abs()
+    assert (off <= slack).all(), f"{int((off > slack).sum())} of {off.numel()} off, at most {float((off / slack).max())}"
+
+
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,N,K", SHAPES)
+def test_non_finite(zs, T, N, K, kind, aligned):
+    """A NaN scale makes every weight's gradient NaN; an infinite or NaN dy those of its output."""
+    rng = np.random.default_rng(T * 3 + N)
+    dy, x, sx = activations(rng, T, N).to(DT[kind]).cuda(), random_codes(rng, T, K).cuda(), random_scales(rng, T).cuda()
+    dw = torch.empty(N, K, device="cuda")
+    for row in (0, T // 2, T - 1):
+        s2, x2 = sx.clone(), x.clone()
+        s2[row] = float("nan")
+        x2[row] = 0  # as a save leaves such a row
+        bdy, bx = operands(dy, x2, aligned)
+        zs.q8_weight_grad(bdy, bx, s2, dw)
+        assert torch.isnan(dw).all(), row
+    others = torch.ones(N, dtype=torch.bool, device="cuda")
+    others[[2, N - 1]] = False
+    for row in (0, T - 1):
+        d2, x2 = dy.clone(), x.clone()
+        d2[row, 2], d2[row, N - 1] = -float("inf"), float("nan")
+        x2[row] = 7
+        bdy, bx = operands(d2, x2, aligned)
+        zs.q8_weight_grad(bdy, bx, sx, dw)
+        assert (torch.isinf(dw[2]) & (dw[2] < 0)).all() and torch.isnan(dw[N - 1]).all(), row
+        assert torch.isfinite(dw[others]).all(), row
+
+
+# tokens split over waves, tiles of 64 at any address, tiles of 128 and of 256
+LONG = [(3001, 256, 256), (4097, 70, 90), (5000, 1500, 1530), (8000, 1100, 1300), (4097, 3001, 3203)]
+
+
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,N,K", LONG)
+def test_long_sums_of_small_integers_are_exact(zs, T, N, K, kind, aligned):
+    """Whole numbers whose partial sums stay below 2^24 add up without rounding in fp32, in any order: every token
+    counts once, and all of its bits do.  fp16: odd numbers of 11 bits, whose last three lie in the second bf16 part."""
+    rng = np.random.default_rng(T + K)
+    top = 2 ** 24 // (T * 1) - 1
+    if kind == "fp16":
+        dy = torch.from_numpy(rng.integers(1, min(1024, top // 2), (T, N)) * 2 + 1)
+    else:
+        dy = torch.from_numpy(rng.integers(1, 128, (T, N)))
+    dy = dy * torch.from_numpy(rng.choice((-1, 1), (T, N)))
+    most = max(1, top // (int(dy.abs().max()) + 4))
+    x = torch.from_numpy(rng.integers(-min(most, 127), min(most, 127) + 1, (T, K), dtype=np.int8))
+    assert (int(dy.abs().max()) + 4) * int(x.abs().max()) * T < 2 ** 24
+    held = dy.to(DT[kind])
+    assert torch.equal(held.double(), dy.double())
+    bdy, bx = operands(held.cuda(), x.cuda(), aligned)
+    dw = torch.empty(N, K, device="cuda")
+    zs.q8_weight_grad(bdy, bx, torch.ones(T, device="cuda"), dw)
+    want = dy.cuda().double().t() @ x.cuda().double()
+    assert torch.equal(dw.double(), want), int((dw.double() != want).sum())
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 64, 64), (40, 33, 65), (200, 1500, 1530)])
+def test_the_smallest_values_count(zs, T, N, K):
+    """Subnormal bf16 gradients (2^-133 .. 2^-126) times codes: products and sums of normal size are not lost."""
+    rng = np.random.default_rng(N)
+    dy = torch.from_numpy(rng.integers(1, 128, (T, N))).double() * 2.0 ** -133
+    held = dy.to(torch.bfloat16)
+    assert torch.equal(held.double(), dy)
+    x = torch.from_numpy(rng.integers(64, 128, (T, K), dtype=np.int8))
+    sx = torch.full((T,), 1024.0)
+    dw = torch.empty(N, K, device="cuda")
+    zs.q8_weight_grad(held.cuda(), x.cuda(), sx.cuda(), dw)
+    want = dy.t() @ (x.double() * 1024)
+    assert torch.equal(dw.cpu().double(), want)  # whole numbers of 2^-123 below 2^24 of them
+
+
+# ------------------------------------------------------------------ graphs and repeats at tiled sizes
+@pytest.mark.parametrize("T,N,K", [(200, 1504, 1536), (300, 4104, 3312), (200, 1501, 1531)])
+def test_tiled_layer_replays_and_repeats(zs, T, N, K):
+    rng = np.random.default_rng(20)
+    a = _layer_buffers(rng, T, N, K)
+    e = {k: v.clone() for k, v in a.items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _layer(zs, a)
+    torch.cuda.current_stream().wait_stream(side)
+    _layer(zs, e)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _layer(zs, a)
+    for replay in range(4):
+        x, dy = activations(rng, T, K).to(torch.bfloat16).cuda(), activations(rng, T, N).to(torch.bfloat16).cuda()
+        for b in (a, e):
+            b["x"].copy_(x)
+            b["dy"].copy_(dy)
+        graph.replay()
+        _layer(zs, e)
+        torch.cuda.synchronize()
+        for k in a:
+            assert same_bits(a[k], e[k]), (replay, k)
