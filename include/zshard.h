@@ -431,6 +431,11 @@ ZS_API zs_status zs_cpu_adam(const float* gbar, int64_t n, float* master, float*
  * may interleave, and a vector or a single row may lie between the rows of a
  * matrix; matrices of several rows at different distances are refused where
  * their ranges meet.  Nothing but the outputs' own rows and columns is written.
+ * Of the operands of zs_q8_matmul and zs_q8_weight_grad whose rows start on
+ * 16-byte boundaries, the bytes between one row's end and the next row may be
+ * read too, and up to 3 bytes behind the last row, within its aligned 4-byte
+ * word; whatever they hold, and whatever is written to them meanwhile, reaches
+ * no result.  All other calls read their operands' rows and columns only.
  * No workspace, no allocation; every call enqueues kernels on `stream` only and
  * may be captured.  Results do not depend on what runs beside them, call to
  * call.

@@ -1,6 +1,6 @@
 """The tiled kernels of the 8-bit weight gradient (128 x 128 and 256 x 256, operands loaded to LDS directly or through
-registers) and the split one, at scales that are no power of two, non-finite values, long sums that have to be exact,
-captured graphs and repeated calls.  Plain forms in 64 bits."""
+registers) and the split one, at scales that are no power of two, non-finite values, values around the operands, long
+sums that have to be exact, captured graphs and repeated calls.  Plain forms in 64 bits."""
 import numpy as np
 import pytest
 import torch
@@ -84,6 +84,38 @@ def test_non_finite(zs, T, N, K, kind, aligned):
         zs.q8_weight_grad(bdy, bx, sx, dw)
         assert (torch.isinf(dw[2]) & (dw[2] < 0)).all() and torch.isnan(dw[N - 1]).all(), row
         assert torch.isfinite(dw[others]).all(), row
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,N,K", SHAPES)
+def test_what_lies_between_and_behind_rows_does_not_count(zs, T, N, K, kind):
+    """NaN between dy's rows and behind its last, the least code around the codes, NaN behind the scales: the same
+    bits as among zeros.  The products the same, among codes of both kinds."""
+    rng = np.random.default_rng(T * 5 + K)
+    dy, x, sx = activations(rng, T, N).to(DT[kind]), random_codes(rng, T, K), random_scales(rng, T)
+    w, sw = random_codes(rng, N, K), random_scales(rng, N)
+    results = []
+    for around, code in ((float("nan"), -128), (0.0, 0)):
+        def inside(v, fill, more):
+            wide = torch.full((v.shape[0] + 1, v.shape[1] + more), fill, dtype=v.dtype, device="cuda")
+            view = wide[:-1, :v.shape[1]]
+            view.copy_(v)
+            return view
+
+        bdy, bx = inside(dy, around, 8 + -N % 8), inside(x, code, 16 + -K % 16)
+        bw = inside(w, code, 16 + -K % 16)
+        bs = torch.full((T + 9,), around, device="cuda")
+        bs[:T] = sx
+        dw = torch.empty(N, K, device="cuda")
+        zs.q8_weight_grad(bdy, bx, bs[:T], dw)
+        y = torch.empty(T, N, device="cuda")
+        zs.q8_matmul(bx, bs[:T], bw, sw.cuda(), y)
+        g = inside(random_codes(np.random.default_rng(N), T, N), code, 16 + -N % 16)
+        dx = torch.empty(T, K, device="cuda")
+        zs.q8_matmul(g, bs[:T], bw, None, dx, trans_w=False)
+        results.append((dw, y, dx))
+    for a, b in zip(*results):
+        assert torch.isfinite(a).all() and same_bits(a, b)
 
 
 # tokens split over waves, tiles of 64 at any address, tiles of 128 and of 256
