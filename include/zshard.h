@@ -442,7 +442,11 @@ ZS_API zs_status zs_cpu_adam(const float* gbar, int64_t n, float* master, float*
  *
  * Non-finite values: a row that holds a NaN or an infinity gets the scale NaN
  * and codes 0, so that everything made from it is NaN and a loss scaler that
- * looks at the gradients sees it.
+ * looks at the gradients sees it.  (The values are those that get codes: with
+ * col_scale, the products.)  What is made from finite rows is computed as stated
+ * at each call, and a result past its format's range becomes an infinity; a
+ * saved row that lies within 1% of that range may load as infinities, see
+ * zs_q8_load.
  * ------------------------------------------------------------------------- */
 
 /* Scale rules of zs_q8_save. */
@@ -454,8 +458,9 @@ ZS_API zs_status zs_cpu_adam(const float* gbar, int64_t n, float* master, float*
      ZS_Q8_SCALE_AMAX:  scales[t] = max(f32(a / 127), 2^-126)
      ZS_Q8_SCALE_POW2:  scales[t] = the least power of two, at least 2^-126,
                         with a <= 127 * scales[t].  Such codes times their scale
-                        are exact in bf16, so the weight gradient's operands
-                        are exact too; the step is up to twice as wide.
+                        are exact in bf16 (up to 127 * 2^121: see zs_q8_load),
+                        so the weight gradient's operands are exact too; the
+                        step is up to twice as wide.
      codes[t][k] = the exact v / scales[t] rounded to an integer, ties to even.
    x: rows x cols in x_format (BF16, FP16 or FP32).  col_scale: device fp32
    array of cols, or NULL: folds a scale that lies along the codes' summed axis
@@ -468,7 +473,17 @@ ZS_API zs_status zs_q8_save(const void* x, int32_t x_format, int64_t ld_x, int64
                             float* scales, zs_stream stream);
 
 /* Values of rows of codes: out[t][k] = codes[t][k] * scales[t] (fp32), rounded
-   to out_format (BF16, FP16 or FP32).  Errors as zs_q8_save. */
+   to out_format (BF16, FP16 or FP32).  The code nearest to a value may stand for
+   a larger one, which at the end of a format's range is an infinity:
+     ZS_Q8_SCALE_POW2: in a row whose largest magnitude is above 127 * 2^9 = 65024
+     (fp16; the largest value is 65504) or above 127 * 2^121 (bf16 and fp32:
+     within 0.8% of the largest value), every value from that bound on, since
+     its code is 64 at a scale of 2^10 or 2^122, and 2^16 or 2^128 is past the range.
+     The operand of zs_q8_weight_grad, a bf16, is that infinity too.
+     ZS_Q8_SCALE_AMAX: only fp32's largest value itself, and in bf16 what is
+     nearer to 2^128 than to bf16's largest value.
+   Where such values are met, save them with ZS_Q8_SCALE_AMAX or scaled down.
+   Errors as zs_q8_save. */
 ZS_API zs_status zs_q8_load(const int8_t* codes, int64_t ld_codes, const float* scales, int64_t rows, int64_t cols,
                             void* out, int32_t out_format, int64_t ld_out, zs_stream stream);
 
@@ -494,7 +509,7 @@ ZS_API zs_status zs_q8_matmul(const int8_t* x_codes, int64_t ld_x, const float* 
      dw[n][k] = add[n][k] + sum_t dy[t][n] * (x_codes[t][k] * x_scales[t])
    dy: T x N in dy_format (BF16 or FP16, taken exactly).  x_codes T x K with
    scales, as zs_q8_save wrote them; a code times its scale is rounded to bf16
-   (exact for ZS_Q8_SCALE_POW2).  Sums are fp32.  add: NULL for none, or an
+   (exact for ZS_Q8_SCALE_POW2, up to 127 * 2^121).  Sums are fp32.  add: NULL for none, or an
    N x K matrix in dw's format and with dw's ld, which may be dw itself (the
    sums of earlier micro-batches).  dw: N x K in dw_format (BF16, FP16 or FP32),
    rounded once.  T = 0 writes add, or zeros.  Errors as zs_q8_save. */

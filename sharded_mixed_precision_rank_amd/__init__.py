@@ -874,7 +874,9 @@ def q8_save(x, codes, scales, col_scale=None, rule="pow2", stream=None) -> None:
     ``codes`` and ``scales``: a layer's input kept for the backward pass, a weight's 8-bit working copy (from
     its fp32 master or 16-bit copy; a row is a channel), or an output gradient with the weight's channel scales
     folded in (``col_scale``).  ``rule``: "pow2" (a power of two, exact in the weight gradient) or "amax" (the
-    row's largest magnitude over 127); see zs_q8_save.  Matrices may be views with contiguous rows."""
+    row's largest magnitude over 127); see zs_q8_save.  Matrices may be views with contiguous rows.  With "pow2",
+    values at the very end of their type's range (from 65024 in fp16, 127 * 2^121 in bf16 and fp32) load as
+    infinities; "amax" keeps them finite (fp32's largest value apart)."""
     p, rows, cols, ld, fmt = _matrix(x, _Q8_FORMATS, "x")
     q, qr, qc, qld, _ = _matrix(codes, _Q8_CODES, "codes")
     if qr != rows or qc != cols:

@@ -188,3 +188,51 @@ def test_tiled_layer_replays_and_repeats(zs, T, N, K):
         torch.cuda.synchronize()
         for k in a:
             assert same_bits(a[k], e[k]), (replay, k)
+
+
+# ------------------------------------------------------------------ the end of a type's range
+TOP = 127.0 * 2.0 ** 121
+ROWS = {"fp16": [65024.0, 65056.0, 65088.0, 65504.0],
+        "bf16": [TOP, float(torch.finfo(torch.bfloat16).max)],
+        "fp32": [TOP, TOP * (1 + 2.0 ** -23), 2.0 ** 128 * (1 - 2.0 ** -23)]}
+
+
+@pytest.mark.parametrize("kind", list(ROWS))
+@pytest.mark.parametrize("cols", [6, 70, 5000])
+def test_rows_at_the_end_of_the_range(zs, kind, cols):
+    """Which finite values load as infinities: with powers of two those from 127 * 2^9 (fp16) or 127 * 2^121 (bf16, fp32)
+    on, in rows that hold more than that; with the largest-magnitude rule none."""
+    tops = torch.tensor(ROWS[kind], dtype=torch.float64)
+    border = 65024.0 if kind == "fp16" else TOP
+    shares = torch.linspace(0.5, 1.0, cols, dtype=torch.float64)
+    shares[0] = 0.0
+    x = (tops[:, None] * shares).to(DT[kind])
+    x[:, cols - 1] = tops.to(DT[kind])
+    x[:, 1] = -x[:, cols - 1]
+    x[:, 2] = torch.tensor(border).to(DT[kind])
+    assert torch.isfinite(x).all()
+    rows = len(tops)
+    q, s = torch.empty(rows, cols, dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    out = torch.empty_like(x, device="cuda")
+    for rule in ("pow2", "amax"):
+        zs.q8_save(x.cuda(), q, s, rule=rule)
+        wq, ws = ref.save(x, rule)
+        assert torch.equal(q.cpu(), wq) and same_bits(s, ws)
+        zs.q8_load(q, s, out)
+        got, v = out.cpu().double(), x.double()
+        past = (v.abs() >= border) & (tops[:, None] > border) if rule == "pow2" else torch.zeros_like(v, dtype=torch.bool)
+        assert torch.equal(torch.isinf(got), past), rule
+        assert (got.sign() == v.sign())[past].all()
+        # elsewhere half a step of the scale, and the output's rounding
+        off = (got - v).abs()[~past]
+        assert (off <= (s.cpu().double()[:, None] / 2 + v.abs() * 2 * ref.HALF_STEP[kind])[~past]).all()
+    if kind == "bf16":  # the weight gradient's operand: an infinity where the load gives one
+        zs.q8_save(x.cuda(), q, s, rule="pow2")
+        zs.q8_load(q, s, out)
+        dy = torch.full((1, 1), 0.5, dtype=torch.bfloat16, device="cuda")
+        for row in range(rows):
+            dw = torch.empty(1, cols, device="cuda")
+            zs.q8_weight_grad(dy, q[row:row + 1], s[row:row + 1], dw)
+            assert torch.equal(torch.isinf(dw[0]), torch.isinf(out[row]))
+            finite = torch.isfinite(out[row])
+            assert torch.equal(dw[0][finite], out[row][finite].float() * 0.5)
