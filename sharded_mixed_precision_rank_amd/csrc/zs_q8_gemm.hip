@@ -601,7 +601,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
 }
 
 // ---------------------------------------------------------------------------
-// Few rows of x: 16 MT x 16 NT outputs per workgroup, whose W waves each take
+// Few rows of x: 16 x 16 NT outputs per workgroup, whose W waves each take
 // every W-th 64 codes of the summed axis, so that the weight's bytes are
 // spread over many waves although the outputs are few.  No wave needs
 // another's operands: kNT reads fragments from memory straight into
@@ -610,13 +610,14 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
 // order does not matter).  Bound by the weight's bytes: one token, N = 4096: K =
 // 4096 in 6.2 us, 11008 in 10.9 (4.1 TB/s).  kNN, 61 tokens, 4096 x 4096: 10.1 us.
 // ---------------------------------------------------------------------------
-template <Q8Op OP, int MT, int NT, int W>
+template <Q8Op OP, int NT, int W>
 __global__ __launch_bounds__(W * 64, 2) void q8_gemm_split(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {
   constexpr bool kNT = OP == Q8Op::kNT;
-  constexpr int BM = MT * 16, BN = NT * 16;
+  constexpr int BM = 16, BN = NT * 16;
+  static_assert(kNT || NT == 4, "four pieces in a row of b");
   constexpr int kPitch = BN + 4;                       // of the sums in LDS: lanes of an instruction in 64 banks
   constexpr int kSums = BM * kPitch * 4;
-  constexpr int kStageBytes = kNT ? 0 : (MT + NT) * 1024;  // a wave's operands of one step
+  constexpr int kStageBytes = kNT ? 0 : (1 + NT) * 1024;  // a wave's operands of one step
   constexpr int kLds = 2 * W * kStageBytes > kSums ? 2 * W * kStageBytes : kSums;
   __shared__ __attribute__((aligned(1024))) char lds[kLds];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -628,13 +629,11 @@ __global__ __launch_bounds__(W * 64, 2) void q8_gemm_split(const Q8Gemm a, uint3
   const int32_t lda = (int32_t)a.lda, ldb = (int32_t)a.ldb, cols = left_of(a.N, n0, BN);
   const Rsrc ra = make_rsrc((const char*)a.a + m0 * a.lda, left_of(a.M, m0, BM), K, lda);
 
-  i32x4 acc[MT][NT];
+  i32x4 acc[NT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = (i32x4){0, 0, 0, 0};
+  for (int j = 0; j < NT; ++j) acc[j] = (i32x4){0, 0, 0, 0};
   // codes of a past K, in the step that holds its end
-  auto cut = [&](int step, i32x4* fa) {
+  auto cut = [&](int step, i32x4& fa) {
     if (step * 64 + 64 > K) {
       const int left = K - step * 64 - 16 * g;
       i32x4 mask;
@@ -643,20 +642,18 @@ __global__ __launch_bounds__(W * 64, 2) void q8_gemm_split(const Q8Gemm a, uint3
         const int b = left - 4 * d;
         mask[d] = b >= 4 ? -1 : b <= 0 ? 0 : (1 << (8 * b)) - 1;
       }
-#pragma unroll
-      for (int i = 0; i < MT; ++i) fa[i] &= mask;
+      fa &= mask;
     }
   };
   if constexpr (kNT) {
     const Rsrc rb = make_rsrc((const char*)a.b + n0 * a.ldb, cols, K, ldb);
     const uint32_t va = (uint32_t)(i16 * lda + g * 16), vb = (uint32_t)(i16 * ldb + g * 16);
-    constexpr int kAhead = MT * NT >= 16 ? 2 : 4;  // steps in flight
-    i32x4 fa[kAhead][MT], fb[kAhead][NT];
+    constexpr int kAhead = 4;  // steps in flight
+    i32x4 fa[kAhead], fb[kAhead][NT];
     auto fetch = [&](int step, int u) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) fb[u][j] = __builtin_bit_cast(i32x4, ld_buffer16(rb, vb + j * 16 * ldb + step * 64));
-#pragma unroll
-      for (int i = 0; i < MT; ++i) fa[u][i] = __builtin_bit_cast(i32x4, ld_buffer16(ra, va + i * 16 * lda + step * 64));
+      fa[u] = __builtin_bit_cast(i32x4, ld_buffer16(ra, va + step * 64));
     };
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) fetch(wave + u * W, u);
@@ -667,30 +664,26 @@ __global__ __launch_bounds__(W * 64, 2) void q8_gemm_split(const Q8Gemm a, uint3
         if (at < steps) {
           cut(at, fa[u]);
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[u][j], fa[u][i], acc[i][j], 0, 0, 0);
+          for (int j = 0; j < NT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[u][j], fa[u], acc[j], 0, 0, 0);
         }
         fetch(at + kAhead * W, u);
       }
     }
   } else {
-    // a step's rows of a: 64 codes, 4 pieces, piece c of row r at place c ^ (r / 2 % 4); its 64 rows of b: NT
-    // pieces, at place c ^ s(r) where there are four
+    // a step's rows of a: 64 codes, 4 pieces, piece c of row r at place c ^ (r / 2 % 4); its 64 rows of b: four
+    // pieces, at place c ^ s(r)
     const uint32_t mine = (uint32_t)(uintptr_t)(LDS char*)lds + wave * 2 * kStageBytes;
-    auto s_of = [](int r) { return NT == 4 ? (r >> 2 & 1) | (r >> 4 & 1) << 1 : 0; };
+    auto s_of = [](int r) { return (r >> 2 & 1) | (r >> 4 & 1) << 1; };
     const uint32_t va = (uint32_t)((lane >> 2) * lda + ((lane & 3) ^ (lane >> 3 & 3)) * 16);
     auto fetch = [&](int step, int buf) {
       const int32_t k0 = step * 64;
       const Rsrc rb = make_rsrc((const char*)a.b + (int64_t)k0 * a.ldb + n0, K - k0 < 64 ? K - k0 : 64, cols, ldb);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) load_to_lds(ra, va + i * 16 * lda + k0, mine + buf * kStageBytes + i * 1024);
+      load_to_lds(ra, va + k0, mine + buf * kStageBytes);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int row = j * (64 / NT) + lane / NT;
         load_to_lds(rb, (uint32_t)(row * ldb + ((lane % NT) ^ s_of(row)) * 16),
-                    mine + buf * kStageBytes + MT * 1024 + j * 1024);
+                    mine + buf * kStageBytes + 1024 + j * 1024);
       }
     };
     int buf = 0;
@@ -699,28 +692,24 @@ __global__ __launch_bounds__(W * 64, 2) void q8_gemm_split(const Q8Gemm a, uint3
       // what was read from the other buffer has been used
       if (step + W < steps) {
         fetch(step + W, buf ^ 1);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(MT + NT) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(1 + NT) : "memory");
       } else {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       }
       LDS char* p = (LDS char*)lds + wave * 2 * kStageBytes + buf * kStageBytes;
-      i32x4 fa[MT], fb[NT];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) fa[i] = *(LDS i32x4*)(p + i * 1024 + i16 * 64 + (g ^ (i16 >> 1 & 3)) * 16);
+      const i32x4 fa = *(LDS i32x4*)(p + i16 * 64 + (g ^ (i16 >> 1 & 3)) * 16);
+      i32x4 fb[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int row = 16 * g + (i16 >> 1);
-        LDS char* q = p + MT * 1024 + row * BN + (i16 & 1) * 8;
+        LDS char* q = p + 1024 + row * BN + (i16 & 1) * 8;
         const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS i32x2*)(q + (j ^ s_of(row)) * 16));
         const i32x2 y = __builtin_amdgcn_ds_read_tr8_b64_v2i32((LDS i32x2*)(q + 8 * BN + (j ^ s_of(row + 8)) * 16));
         fb[j] = (i32x4){x[0], x[1], y[0], y[1]};
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < NT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa, acc[j], 0, 0, 0);
     }
     __syncthreads();  // the operands' LDS is done with
   }
@@ -728,13 +717,11 @@ __global__ __launch_bounds__(W * 64, 2) void q8_gemm_split(const Q8Gemm a, uint3
   for (int i = tid; i < BM * kPitch; i += W * 64) sums[i] = 0;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        __hip_atomic_fetch_add(&sums[(i * 16 + i16) * kPitch + (j * 4 + r) * 4 + g], acc[i][j][r], __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_WORKGROUP);
+    for (int r = 0; r < 4; ++r)
+      __hip_atomic_fetch_add(&sums[i16 * kPitch + (j * 4 + r) * 4 + g], acc[j][r], __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_WORKGROUP);
   __syncthreads();
   for (int i = tid; i < BM * (BN / 4); i += W * 64) {
     const int row = i / (BN / 4), four = i % (BN / 4);  // columns 4 * four .. + 3: j = four / 4, g = four % 4
@@ -751,10 +738,10 @@ __global__ __launch_bounds__(W * 64, 2) void q8_gemm_split(const Q8Gemm a, uint3
   }
 }
 
-template <Q8Op OP, int MT, int NT, int W>
+template <Q8Op OP, int NT, int W>
 hipError_t split_launch(const Q8Gemm& a, hipStream_t stream) {
-  const uint32_t tm = (uint32_t)((a.M + MT * 16 - 1) / (MT * 16)), tn = (uint32_t)((a.N + NT * 16 - 1) / (NT * 16));
-  q8_gemm_split<OP, MT, NT, W><<<dim3(tm * tn), W * 64, 0, stream>>>(a, tm, tn);
+  const uint32_t tm = (uint32_t)((a.M + 15) / 16), tn = (uint32_t)((a.N + NT * 16 - 1) / (NT * 16));
+  q8_gemm_split<OP, NT, W><<<dim3(tm * tn), W * 64, 0, stream>>>(a, tm, tn);
   return hipGetLastError();
 }
 
@@ -824,9 +811,9 @@ hipError_t product_launch(const Q8Gemm& given, hipStream_t stream) {
   // kNN, tiles of 16 x 64: 61 tokens 10.1 / 13.4 for 4096 columns (256 tiles), 21.0 / 14.2 for 11008 (688); 16 tokens
   // 11.2 / 12.3 for 11008 (172), 32 tokens 17.1 / 12.7 (344).
   if constexpr (OP == Q8Op::kNT) {
-    if (a.M <= 16 && (a.N + 63) / 64 <= 96) return split_launch<OP, 1, 1, 4>(a, stream);
+    if (a.M <= 16 && (a.N + 63) / 64 <= 96) return split_launch<OP, 1, 4>(a, stream);
   } else {
-    if (tiles_of(a, 16, 64) <= 256) return split_launch<OP, 1, 4, 8>(a, stream);
+    if (tiles_of(a, 16, 64) <= 256) return split_launch<OP, 4, 8>(a, stream);
   }
   switch (tile_for(a)) {
     case Tile::k64: return tile_launch<OP, 64, 64, 4, 1, 4>(a, stream);
