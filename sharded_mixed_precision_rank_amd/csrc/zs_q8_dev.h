@@ -29,7 +29,7 @@ __device__ __forceinline__ void st_any(E* p, V v) {
   typedef V U __attribute__((aligned(__alignof__(E))));
   *(GLB U*)(GLB E*)p = v;
 }
-// The same past the caches' normal order: for outputs much larger than them.
+// The same past the caches' normal order: for outputs that would push operands out of them.
 template <class V, class E>
 __device__ __forceinline__ void st_past(E* p, V v) {
   typedef V U __attribute__((aligned(__alignof__(E))));

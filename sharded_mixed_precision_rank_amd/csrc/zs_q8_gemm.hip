@@ -131,7 +131,9 @@ __device__ __forceinline__ void trade(uint32_t x, uint32_t y, uint32_t& lo, uint
 // operands staged through registers 16 bytes at a time, so that rows may start
 // at any address and end anywhere.  The first operand of the matrix
 // instruction is b's, so that a lane ends with four consecutive columns of a
-// row.  8192 x 11008 x 4096: 794 us, kNN 1392, kTN 2079.
+// row.  8192 x 11008 x 4096 with rows one byte off 16-byte boundaries: 1172 us,
+// kNN 2058 (on them, by the tiled kernels, 338 and 291): loads of 16 bytes that
+// straddle lines, one buffer and two barriers a step.
 // ---------------------------------------------------------------------------
 constexpr int kAnyTile = 64;
 constexpr int kAnyK = 128;   // codes along K per step (kNT, kNN)
@@ -294,13 +296,13 @@ hipError_t any_launch(const Q8Gemm& a, hipStream_t stream) {
 // wave has read all of the stage and its part of the next one has landed.
 //
 // 256 x 256 by eight waves (128 x 64 each, 245 registers, 128 KB of LDS):
-// 8192 x 11008 x 4096 in 314-330 us (2240-2350 TOP/s), its input gradient in 282-287
-// (2580-2620), where a library's int8 product takes 357 (2071).  Of 119 us at
+// 8192 x 11008 x 4096 in 315-356 us (2070-2350 TOP/s), its input gradient in 275-297
+// (2490-2690), where a library's int8 product takes 362 (2040).  Of 119 us at
 // 8192 x 4096 x 4096, the matrix instructions alone take 79 (the clock falls
 // under them, to about 1.7 GHz) and the loads alone 102.  Four waves of 128 x
 // 128 spill or shuffle accumulators (309-909 us); stages of 64 codes in a ring of
 // four or five load half lines and are slower (125 against 119, kNN 156 against
-// 125).  Bank conflicts: none, by counter.
+// 125).  Bank conflicts: none, by counter (SQ_LDS_BANK_CONFLICT, every tile shape).
 // ---------------------------------------------------------------------------
 typedef uint32_t Rsrc __attribute__((ext_vector_type(4)));
 
@@ -608,7 +610,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_gemm_tile(const Q8Gemm a, u
 // registers; kNN moves them through a part of LDS of the wave's own, to turn
 // the weight's rows.  The waves' sums meet in LDS (integer additions, whose
 // order does not matter).  Bound by the weight's bytes: one token, N = 4096: K =
-// 4096 in 6.2 us, 11008 in 10.9 (4.1 TB/s).  kNN, 61 tokens, 4096 x 4096: 10.1 us.
+// 4096 in 6.1 us, 11008 in 10.8 (4.2 TB/s).  kNN, 61 tokens, 4096 x 4096: 10.4 us.
 // ---------------------------------------------------------------------------
 template <Q8Op OP, int NT, int W>
 __global__ __launch_bounds__(W * 64, 2) void q8_gemm_split(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {
@@ -748,9 +750,12 @@ hipError_t split_launch(const Q8Gemm& a, hipStream_t stream) {
 template <Q8Op OP, int BM, int BN, int WM, int WN, int NS>
 hipError_t tile_launch(const Q8Gemm& a, hipStream_t stream) {
   const uint32_t tm = (uint32_t)((a.M + BM - 1) / BM), tn = (uint32_t)((a.N + BN - 1) / BN);
-  // Large 16-bit outputs otherwise push the operands out of the caches (8192 x 11008 x 4096: 314 us against 361, 8192 x
-  // 4096 x 4096: 122 against 136, kNN 115 against 125; weight gradients, smaller beside their operands, gain 1% or lose
-  // 2%).  Pieces that are not whole 64 bytes lose by it: 1000 x 5003 in fp32, 25.8 us against 18.7.
+  // 16-bit outputs in whole pieces of 64 bytes go past the caches, whatever their size: large ones otherwise push the
+  // operands out of them (8192 x 11008 x 4096: 314 us against 361 when this was chosen, 8192 x 4096 x 4096: 122 against
+  // 136, kNN 115 against 125), and smaller ones gain too, alone (4096 x 4096 x 4096: 58.0 against 61.7, 1000: 22.5 against
+  // 23.7).  With a call behind them that reads the output, elementwise, the two together: 4096 x 4096 x 4096 68.5 against
+  // 70.1 us, 2000 41.7 both, 1000 (8 MB) 27.5 against 26.4.  Weight gradients, smaller beside their operands, gain 1% or
+  // lose 2%.  Pieces that are not whole 64 bytes lose by it: 1000 x 5003 in fp32, 25.8 us against 18.7.
   if constexpr (BM >= 128) {
     if (a.format != ZS_FORMAT_FP32 && ((uintptr_t)a.d | (uintptr_t)(a.ldd * 2)) % 64 == 0) {
       q8_gemm_tile<OP, BM, BN, WM, WN, NS, true><<<dim3(tm * tn), WM * WN * 64, 0, stream>>>(a, tm, tn);
@@ -771,14 +776,15 @@ int64_t tiles_of(const Q8Gemm& a, int64_t bm, int64_t bn) { return (a.M + bm - 1
 constexpr int64_t kMostTiles = 1 << 22;
 
 // The tile of a product with 16-byte rows, by the time of one stage of 128
-// codes that its grid needs in all, measured on 256 compute units at K = 4096
-// and 11008 (us):
+// codes that its grid needs in all, measured at K = 4096 and 11008 (us).  The
+// rounds are of the MI355X's 256 compute units, here and in the rules below:
 //   256 x 256, one workgroup a unit: 1.15-1.45 for a first round of up to 256
 //     tiles, 1.7-1.9 a round where there are more;
 //   128 x 128: 0.45-0.7 up to 256 tiles with four stages, beyond that two
 //     workgroups of two stages a unit, 0.8-1.15 for each 512;
-//   96 x 64: 0.36-0.40 up to 256 tiles; beyond that one of the others is as
-//     good or better (640 x 4096: 19.5 us, 128 x 128 18.2);
+//   96 x 64: 0.36-0.40 up to 256 tiles, less than any other where 64 x 64 need
+//     a second round; beyond 256 one of the others is as good or better (640 x
+//     4096: 19.5 us, 128 x 128 18.2);
 //   64 x 64: 0.25-0.33 up to 256 tiles, 0.45-0.5 for each 512.
 // For example 8192 x 11008 by 4096: 346 / 407 / 616 us; 2000 x 4096: 44.7 /
 // 36.2 / 59.5; 1000 x 4096: 42.4 / 21.8 / 31.2; 333 x 4096: 41.5 / 16.5 /
@@ -807,7 +813,10 @@ hipError_t product_launch(const Q8Gemm& given, hipStream_t stream) {
   if (a.M <= 1) a.lda = (a.K + 15) / 16 * 16;
   if (rows_b <= 1) a.ldb = OP == Q8Op::kNT ? (a.K + 15) / 16 * 16 : 256;
   // Few rows: their tiles of 64 columns may be too few to draw on all of the memory.  kNT, K = 4096: one token 6.2 us
-  // against 9.2 in 64 x 64 tiles for N = 4096, 11.8 against 10.0 for N = 11008; 16 tokens 7.8 / 9.4 and 16.3 / 9.8.
+  // against 9.2 in 64 x 64 tiles for N = 4096, 11.8 against 10.0 for N = 11008; 16 tokens 7.8 / 9.4 and 16.3 / 9.8.  From
+  // 17 tokens on the split kernel's rows of tiles read the weight again: 17 and 61 tokens, 4096 x 4096: 11.3 and 20.0 us
+  // against 10.1 and 10.3; 4096 x 11008: 23.4 and 44.0 against 21.5 and 21.8 (only a weight too narrow for that would
+  // gain: 1024 x 11008, 12.9 and 13.0 against 21.2 and 21.4).
   // kNN, tiles of 16 x 64: 61 tokens 10.1 / 13.4 for 4096 columns (256 tiles), 21.0 / 14.2 for 11008 (688); 16 tokens
   // 11.2 / 12.3 for 11008 (172), 32 tokens 17.1 / 12.7 (344).
   if constexpr (OP == Q8Op::kNT) {
@@ -835,13 +844,16 @@ hipError_t product_launch(const Q8Gemm& given, hipStream_t stream) {
 // is (kThrough).  kDirect and kParts want rows on 16-byte boundaries, the others
 // take any.
 //
-// kDirect, 256 x 256: T, N, K = 8192, 11008, 4096 in 600-640 us (1150-1230
-// TFLOP/s; a library's bf16 product of the same layout 797), 8192, 4096, 4096 in
-// 236.  Of those 236, the matrix instructions take 136 and with the fragments'
-// reads 181; the codes' fetch adds 30, dy's loads 17, the conversion 8: a fetch
-// waits on memory for more than the stage that it has.  Slower: 32-token stages
-// in a ring of four with the codes loaded to LDS as they are (256); the waves in
-// two groups half a stage apart (311); the codes fetched after dy's loads (284).
+// kDirect, 256 x 256: T, N, K = 8192, 11008, 4096 in 619-699 us (1060-1190
+// TFLOP/s; a library's bf16 product of the same layout 795), 8192, 4096, 4096 in
+// 224-269.  Of 236 for the latter, the matrix instructions took 136 and with the
+// fragments' reads 181; the codes' fetch added 30, dy's loads 17, the conversion 8:
+// a fetch waits on memory for more than the stage that it has.  Slower: 32-token
+// stages in a ring of four with the codes loaded to LDS as they are (256); the
+// waves in two groups half a stage apart (311); the codes fetched after dy's loads,
+// with the same wait for all of them (284).  Bank conflicts of the transposing
+// reads are 20-25% of the LDS cycles.  kParts (fp16) 1228-1288; rows one element
+// off, 8192, 4096, 4096: kThrough 409-433, kPartsAny 669-692.
 // ---------------------------------------------------------------------------
 enum class DyPath { kDirect, kParts, kThrough, kPartsAny };
 
@@ -1075,8 +1087,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void q8_grad_tile(const Q8Gemm a, u
 // each take every eighth 32 tokens, with a part of LDS of their own that they
 // load three steps ahead and read through transposing reads: no wave waits for
 // another until their sums are added, in the waves' order.  The codes become
-// bf16 in the fragments: no other wave needs them.  T, N, K = 8192, 256, 256: 28
-// us (in 128 x 128 tiles 105), bound by the loads' latency.
+// bf16 in the fragments: no other wave needs them.  T, N, K = 8192, 256, 256: 26
+// us (in 128 x 128 tiles 105), bound by the loads' latency on the 16 compute
+// units that 16 workgroups use.
 // ---------------------------------------------------------------------------
 template <bool TWO>
 __global__ __launch_bounds__(512, 2) void q8_grad_split(const Q8Gemm a, uint32_t tiles_m, uint32_t tiles_n) {
@@ -1213,7 +1226,7 @@ hipError_t grad_tile_launch(const Q8Gemm& a, hipStream_t stream) {
 
 // The weight gradient's kernel, by the time its grid needs for T tokens, in
 // stages of 64 (us, measured on 256 compute units at T = 1 to 16384; fp16, whose
-// stages are 32 tokens, takes about 1.8 times as long in each):
+// stages are 32 tokens, takes 1.7 to 2 times as long in each):
 //   64 x 64, tokens split over eight waves: 3.5 and 0.25 a stage for each 256
 //   128 x 128: 4.5 and 0.85 a stage up to 256 tiles, 1.12 for each 512
 //   256 x 256: 8 and 1.4 a stage up to 128 tiles, 1.85 for each 256

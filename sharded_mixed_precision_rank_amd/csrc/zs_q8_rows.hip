@@ -9,9 +9,11 @@
 // load reads a byte and writes a value.  A row is taken by 8 to 64 lanes of a
 // wave, or by a workgroup, that keep it in registers, as it was stored,
 // between the maximum and the codes (rows of more than 16,384 columns are read
-// twice).  16384 x 11008 bf16: save 103-127 us (4.3-5.3 TB/s; a large copy moves
-// 4.9), with column factors 124, load 88-106 (5.1-6.2 TB/s).  Holding the unpacked
-// values took 264 registers and 225-327 us.
+// twice).  16384 x 11008 bf16, other rows at each call: save 123-131 us (4.1-4.4
+// TB/s), load 86-90 (6.0-6.3); a large copy moves 6.3.  The same rows again, part of
+// them in the caches: save 103-110, with column factors 127-153.  The save waits for
+// a whole row, then for its maximum, before it stores: that is what it has over
+// the load.  Holding the unpacked values took 264 registers and 225-327 us.
 #include "zs_q8_dev.h"
 
 namespace zs {
