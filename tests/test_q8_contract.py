@@ -2,8 +2,13 @@
 import os
 import random
 import re
+import shutil
+import subprocess
+
+import pytest
 
 import sharded_mixed_precision_rank_amd as zs
+from sharded_mixed_precision_rank_amd import build
 
 LIB = zs.library()
 A = 0x7F0000000000  # never dereferenced: every call here fails before any HIP call
@@ -43,6 +48,57 @@ def test_loads_to_lds_take_m0_as_an_operand():
                 assert '"{m0}"' in text, (name, instruction)
                 found += 1
     assert found == 2
+
+
+def _scalars(text):
+    """Numbers of the scalar registers named in an instruction's operands."""
+    out = set()
+    for lo, hi, one in re.findall(r"\bs\[(\d+):(\d+)\]|\bs(\d+)\b", text):
+        out |= {int(one)} if one else set(range(int(lo), int(hi) + 1))
+    return out
+
+
+def too_early(listing):
+    """Memory instructions that read a scalar register less than five wait states after a vector instruction wrote it
+    (in the listing's order; a label starts afresh)."""
+    written, bad = [], []
+    for line in listing.splitlines():
+        text = line.split(";")[0].strip()
+        if re.match(r"^[\w.$]+:", text):
+            written = []
+        if not text or text.startswith(".") or text.endswith(":"):
+            continue
+        op, _, operands = text.partition(" ")
+        if op.startswith(("buffer_", "global_", "flat_", "scratch_")):
+            used = _scalars(operands)
+            if any(used & regs for _, regs in written):
+                bad.append(text)
+        states = int(operands, 0) + 1 if op == "s_nop" else 1
+        written = [(age + states, regs) for age, regs in written if age + states < 5]
+        if op.startswith("v_"):
+            regs = _scalars(operands.split(",")[0])
+            if regs:
+                written.append((0, regs))
+    return bad
+
+
+def test_too_early_finds_what_it_looks_for():
+    early = "k:\n\tv_readfirstlane_b32 s4, v0\n\ts_mov_b32 m0, s9\n\ts_nop 0\n\tbuffer_load_dwordx4 v1, s[4:7], 0 offen lds\n"
+    assert len(too_early(early)) == 1
+    assert not too_early(early.replace("s_nop 0", "s_nop 3")) and not too_early(early.replace("s4, v0", "s8, v0"))
+
+
+@pytest.mark.skipif(shutil.which("hipcc") is None, reason="no hipcc")
+def test_no_load_takes_a_descriptor_just_written_by_a_vector_instruction(tmp_path):
+    """The compiler keeps that distance for its own instructions, not for those in asm statements: the listing of the
+    kernels that load to LDS."""
+    out = str(tmp_path / "gemm.s")
+    flags = [f for f in build.FLAGS if f != "-shared"]
+    subprocess.run(["hipcc", *flags, "-S", "--cuda-device-only", "-x", "hip", os.path.join(CSRC, "zs_q8_gemm.hip"), "-o", out],
+                   check=True, stdout=subprocess.DEVNULL, stderr=subprocess.DEVNULL)
+    listing = open(out, encoding="utf-8").read()
+    assert listing.count(" lds\n") > 100
+    assert not too_early(listing)
 
 
 def _shared(a, b):
