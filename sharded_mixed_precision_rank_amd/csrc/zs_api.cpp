@@ -15,7 +15,7 @@
 
 #include "zs_cpu_adam.h"
 #include "zs_internal.h"
-#include "zs_q8.h"
+#include "zs_matrix_args.h"
 #include "zs_twopass.h"
 
 namespace {

@@ -55,10 +55,4 @@ hipError_t launch_q8_save(const Q8Save& a, hipStream_t stream);
 hipError_t launch_q8_load(const Q8Load& a, hipStream_t stream);
 hipError_t launch_q8_gemm(Q8Op op, const Q8Gemm& a, hipStream_t stream);
 
-// From zs_api.cpp: a status with its thread-local detail string ("" clears
-// it), and the common end of a call that launched something.
-zs_status api_fail(zs_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-void api_clear();
-zs_status api_after_launch(hipError_t e, hipStream_t stream, const char* what);
-
 }  // namespace zs
