@@ -1,13 +1,16 @@
 """Builds libzshard.so (gfx950) in place with hipcc."""
+import concurrent.futures
 import os
 import subprocess
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libzshard.so")
-# Device code and HIP-runtime host code compile as HIP in one hipcc command.
+# Device code and HIP-runtime host code, compiled as HIP, one object a source.
 SOURCES = [os.path.join(CSRC, f) for f in ("zs_kernels.hip", "zs_twopass.hip", "zs_q8_rows.hip", "zs_q8_gemm.hip",
-                                           "zs_api.cpp", "zs_offload.cpp", "zs_q8.cpp")]
+                                           "zs_glu_rows.hip", "zs_glu_gemm.hip", "zs_api.cpp", "zs_offload.cpp", "zs_q8.cpp",
+                                           "zs_glu.cpp")]
 # The host AdamW is plain C++ built by the host compiler into an object that
 # the hipcc link takes as is (its AVX2 path is chosen at run time).  Compiling
 # it as a C++ input inside the hipcc command produced a library that crashed
@@ -15,7 +18,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("zs_kernels.hip", "zs_twopass.hip", "
 HOST_SOURCES = [os.path.join(CSRC, "zs_cpu_adam.cpp")]
 HOST_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-ffp-contract=off", "-fno-fast-math", "-Wall"]
 FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",
     # one rounding per operation, correctly rounded divide and sqrt
     "-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt",
     # no packed fp32 instructions
@@ -24,13 +27,8 @@ FLAGS = [
 ]
 
 
-def _hipcc(sources, objs, out, extra, verbose):
-    cmd = ["hipcc", *FLAGS, *extra]
-    for src in sources:
-        cmd += ["-x", "hip", src]
-    if objs:
-        cmd += ["-x", "none", *objs]
-    cmd += ["-o", out]
+def _hipcc(args, verbose):
+    cmd = ["hipcc", *FLAGS, *args]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -51,7 +49,16 @@ def build(verbose: bool = False, out: str = LIB, extra=()) -> str:
             print(" ".join(hcmd), flush=True)
         subprocess.run(hcmd, check=True)
         objs.append(obj)
-    _hipcc(SOURCES, objs, out, extra, verbose)
+    # one object a source, side by side, then one link
+    with tempfile.TemporaryDirectory() as tmp:
+        def compile_one(src):
+            obj = os.path.join(tmp, os.path.basename(src) + ".o")
+            _hipcc([*extra, "-c", "-x", "hip", src, "-o", obj], verbose)
+            return obj
+
+        with concurrent.futures.ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            device = list(pool.map(compile_one, SOURCES))
+        _hipcc([*device, *objs, "-shared", "-o", out], verbose)
     return out
 
 
