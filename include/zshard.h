@@ -517,6 +517,74 @@ ZS_API zs_status zs_q8_weight_grad(const void* dy, int32_t dy_format, int64_t ld
                                    int64_t ld_x, const float* x_scales, int64_t T, int64_t N, int64_t K,
                                    const void* add, void* dw, int32_t dw_format, int64_t ld_dw, zs_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * The gated feed-forward block and its backward pass, in 16 bits.
+ *
+ *   forward   gate = x Wg^T,  up = x Wu^T,  h = act(gate) * up
+ *   backward  dgate = dh * up * act'(gate),  dup = dh * act(gate)
+ *             dx = dgate Wg + dup Wu
+ *             dWg = dgate^T x,  dWu = dup^T x
+ *
+ * x: T x K (T tokens), Wg and Wu: N x K, gate, up and h: T x N.  Every operand
+ * is bf16 or fp16 (`format`); sums and activations are fp32, and every output is
+ * rounded once, from fp32.  The backward pass takes gate and up as the forward
+ * pass kept them, in 16 bits; dgate and dup are held in 16 bits too, so dx and
+ * the weight gradients carry that rounding beside their own.  The weight
+ * gradients are the chunks that zs_reduce_adam_* and zs_reduce_muon average, or
+ * are added to earlier micro-batches' sums.
+ *
+ * Matrices are row-major with unit column stride; ld is the distance between
+ * rows in elements (at least the columns; not looked at for a single row); the
+ * two weights share one, and so do gate and up, dgate and dup, and dw_gate,
+ * dw_up and what is added to them.  A weight that holds gate and up one behind
+ * the other is two matrices in one buffer.  Any alignment of the elements works;
+ * rows that start on 16-byte boundaries (base and ld) run fastest.  Dimensions
+ * are 0 .. 2^31 - 1; sums of nothing are zeros.  Which bytes outputs may share
+ * and which bytes around the products' operands may be read is as for the 8-bit
+ * operators above.  No workspace, no allocation; every call enqueues one kernel
+ * on `stream` only and may be captured.  Results do not depend on what runs
+ * beside them, call to call.
+ *
+ * Non-finite values spread as the formulas have it; a result past its format's
+ * range becomes an infinity.
+ * ------------------------------------------------------------------------- */
+
+/* Activations (v: a value of gate). */
+#define ZS_ACT_SILU 0      /* v / (1 + e^-v) */
+#define ZS_ACT_GELU 1      /* v (1 + erf(v / sqrt 2)) / 2 */
+#define ZS_ACT_GELU_TANH 2 /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */
+#define ZS_ACT_RELU 3      /* max(v, 0); its slope at 0 is 0 */
+
+/* h = act(x Wg^T) * (x Wu^T), both projections and the product in one kernel.
+   gate and up: T x N, written where given (both or neither), for the backward
+   pass; h is made from the unrounded sums.  h, gate and up share no byte.
+   Errors: ZS_ERR_NULL, ZS_ERR_RANGE, ZS_ERR_ALIGN, ZS_ERR_ALIAS, ZS_ERR_HIP. */
+ZS_API zs_status zs_glu_forward(const void* x, int64_t ld_x, const void* w_gate, const void* w_up, int64_t ld_w,
+                                int32_t format, int64_t T, int64_t N, int64_t K, int32_t act, void* h, int64_t ld_h,
+                                void* gate, void* up, int64_t ld_gu, zs_stream stream);
+
+/* dgate = dh * up * act'(gate), dup = dh * act(gate).  h: NULL, or where
+   act(gate) * up is written again, so that it need not be kept for the gradient
+   of the projection behind it.  dgate may be gate itself, dup up itself and h dh
+   itself (the same address and ld).  Errors as zs_glu_forward. */
+ZS_API zs_status zs_glu_backward(const void* dh, int64_t ld_dh, const void* gate, const void* up, int64_t ld_gu,
+                                 int32_t format, int64_t T, int64_t N, int32_t act, void* dgate, void* dup, int64_t ld_d,
+                                 void* h, int64_t ld_h, zs_stream stream);
+
+/* dx = dgate Wg + dup Wu, one sum.  Errors as zs_glu_forward. */
+ZS_API zs_status zs_glu_input_grad(const void* dgate, const void* dup, int64_t ld_d, const void* w_gate, const void* w_up,
+                                   int64_t ld_w, int32_t format, int64_t T, int64_t N, int64_t K, void* dx,
+                                   int64_t ld_dx, zs_stream stream);
+
+/* dw_gate = add_gate + dgate^T x, dw_up = add_up + dup^T x, in dw_format (BF16,
+   FP16 or FP32), rounded once.  add_gate and add_up: both NULL, or both N x K in
+   dw's format and with dw's ld, which may be dw_gate and dw_up themselves.  T = 0
+   writes what is added, or zeros.  Errors as zs_glu_forward. */
+ZS_API zs_status zs_glu_weight_grad(const void* dgate, const void* dup, int64_t ld_d, const void* x, int64_t ld_x,
+                                    int32_t format, int64_t T, int64_t N, int64_t K, const void* add_gate,
+                                    const void* add_up, void* dw_gate, void* dw_up, int32_t dw_format, int64_t ld_dw,
+                                    zs_stream stream);
+
 /* Workgroups per launch for all later step calls in this process: 0 picks
    automatically from the device's compute-unit count.  Results do not depend
    on it (every element is computed by one thread with the same operations). */

@@ -157,9 +157,20 @@ _lib.zs_q8_matmul.restype = ctypes.c_int
 _lib.zs_q8_matmul.argtypes = [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i32, _i64, _vp]
 _lib.zs_q8_weight_grad.restype = ctypes.c_int
 _lib.zs_q8_weight_grad.argtypes = [_vp, _i32, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp]
+_lib.zs_glu_forward.restype = ctypes.c_int
+_lib.zs_glu_forward.argtypes = [_vp, _i64, _vp, _vp, _i64, _i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _i64, _vp]
+_lib.zs_glu_backward.restype = ctypes.c_int
+_lib.zs_glu_backward.argtypes = [_vp, _i64, _vp, _vp, _i64, _i32, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _vp]
+_lib.zs_glu_input_grad.restype = ctypes.c_int
+_lib.zs_glu_input_grad.argtypes = [_vp, _vp, _i64, _vp, _vp, _i64, _i32, _i64, _i64, _i64, _vp, _i64, _vp]
+_lib.zs_glu_weight_grad.restype = ctypes.c_int
+_lib.zs_glu_weight_grad.argtypes = [_vp, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _i64,
+                                    _vp]
+
 
 FORMATS = {"bf16": 0, "fp16": 1}
 Q8_SCALES = {"amax": 0, "pow2": 1}
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 
 
 class ZShardError(RuntimeError):
@@ -943,6 +954,98 @@ def q8_weight_grad(dy, x_codes, x_scales, dw, add=None, stream=None) -> None:
             raise ValueError(f"add has row stride {ald}, dw {wld}")
     _q8_call(_lib.zs_q8_weight_grad, "zs_q8_weight_grad", used,
              (dp, dfmt, dld, xp, xld, s, T, N, K, ap, wp, fmt, wld), stream)
+
+
+# ------------------------------------------------------------ gated feed-forward block
+def _like(t, other, name, want):
+    """(address, row stride) of a matrix with the shape ``want`` and ``other``'s dtype."""
+    p, rows, cols, ld, _ = _matrix(t, {other.dtype: 0}, name)
+    if (rows, cols) != want:
+        _q8_shape(name, rows, cols, *want)
+    return p, ld
+
+
+def _pair(a, b, names, other, want):
+    """(address, address, row stride) of two matrices that share a shape, a dtype and a row stride."""
+    p, ld = _like(a, other, names[0], want)
+    q, ld2 = _like(b, other, names[1], want)
+    if ld != ld2 and want[0] > 1:
+        raise ValueError(f"{names[0]} has row stride {ld}, {names[1]} {ld2}")
+    return p, q, ld
+
+
+def _act(name) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {tuple(ACTIVATIONS)}, not {name!r}")
+    return ACTIVATIONS[name]
+
+
+def glu_forward(x, w_gate, w_up, h, gate=None, up=None, act="silu", stream=None) -> None:
+    """``h`` (T x N) = act(x w_gate^T) * (x w_up^T), one kernel.  ``x``: T x K, the weights N x K, all bf16 or all
+    fp16.  ``gate`` and ``up`` (both or neither): the projections, kept for :func:`glu_backward`.  ``act``: "silu",
+    "gelu", "gelu_tanh" or "relu"; see zs_glu_forward."""
+    xp, T, K, xld, fmt = _matrix(x, _Q8_DY, "x")
+    N = w_gate.shape[0] if isinstance(w_gate, torch.Tensor) and w_gate.dim() == 2 else -1
+    gp, upp, wld = _pair(w_gate, w_up, ("w_gate", "w_up"), x, (N, K))
+    hp, hld = _like(h, x, "h", (T, N))
+    kg = ku = None
+    kld, used = 0, (x, w_gate, w_up, h)
+    if (gate is None) != (up is None):
+        raise ValueError("gate and up must be given together")
+    if gate is not None:
+        kg, ku, kld = _pair(gate, up, ("gate", "up"), x, (T, N))
+        used = (x, w_gate, w_up, h, gate, up)
+    _q8_call(_lib.zs_glu_forward, "zs_glu_forward", used,
+             (xp, xld, gp, upp, wld, fmt, T, N, K, _act(act), hp, hld, kg, ku, kld), stream)
+
+
+def glu_backward(dh, gate, up, dgate, dup, h=None, act="silu", stream=None) -> None:
+    """``dgate`` = dh * up * act'(gate) and ``dup`` = dh * act(gate) (all T x N, bf16 or fp16), from what
+    :func:`glu_forward` kept.  ``h``: where act(gate) * up is written again.  ``dgate`` may be ``gate`` itself, ``dup``
+    ``up`` and ``h`` ``dh``; see zs_glu_backward."""
+    dp, T, N, dld, fmt = _matrix(dh, _Q8_DY, "dh")
+    gp, upp, gld = _pair(gate, up, ("gate", "up"), dh, (T, N))
+    dgp, dupp, ddld = _pair(dgate, dup, ("dgate", "dup"), dh, (T, N))
+    hp, hld, used = None, 0, (dh, gate, up, dgate, dup)
+    if h is not None:
+        hp, hld = _like(h, dh, "h", (T, N))
+        used = (dh, gate, up, dgate, dup, h)
+    _q8_call(_lib.zs_glu_backward, "zs_glu_backward", used,
+             (dp, dld, gp, upp, gld, fmt, T, N, _act(act), dgp, dupp, ddld, hp, hld), stream)
+
+
+def glu_input_grad(dgate, dup, w_gate, w_up, dx, stream=None) -> None:
+    """``dx`` (T x K) = dgate w_gate + dup w_up, one sum; see zs_glu_input_grad."""
+    _, T, N, _, fmt = _matrix(dgate, _Q8_DY, "dgate")
+    dgp, dupp, dld = _pair(dgate, dup, ("dgate", "dup"), dgate, (T, N))
+    K = w_gate.shape[1] if isinstance(w_gate, torch.Tensor) and w_gate.dim() == 2 else -1
+    gp, upp, wld = _pair(w_gate, w_up, ("w_gate", "w_up"), dgate, (N, K))
+    xp, xld = _like(dx, dgate, "dx", (T, K))
+    _q8_call(_lib.zs_glu_input_grad, "zs_glu_input_grad", (dgate, dup, w_gate, w_up, dx),
+             (dgp, dupp, dld, gp, upp, wld, fmt, T, N, K, xp, xld), stream)
+
+
+def glu_weight_grad(dgate, dup, x, dw_gate, dw_up, add_gate=None, add_up=None, stream=None) -> None:
+    """``dw_gate`` = ``add_gate`` + dgate^T x and ``dw_up`` = ``add_up`` + dup^T x (N x K; bf16, fp16 or fp32), one
+    kernel.  What is added (both or neither) has the outputs' dtype and row stride and may be the outputs themselves;
+    see zs_glu_weight_grad."""
+    _, T, N, _, fmt = _matrix(dgate, _Q8_DY, "dgate")
+    dgp, dupp, dld = _pair(dgate, dup, ("dgate", "dup"), dgate, (T, N))
+    K = x.shape[1] if isinstance(x, torch.Tensor) and x.dim() == 2 else -1
+    xp, xld = _like(x, dgate, "x", (T, K))
+    _, _, _, _, wfmt = _matrix(dw_gate, _Q8_FORMATS, "dw_gate")
+    gp, upp, wld = _pair(dw_gate, dw_up, ("dw_gate", "dw_up"), dw_gate, (N, K))
+    ag = au = None
+    used = (dgate, dup, x, dw_gate, dw_up)
+    if (add_gate is None) != (add_up is None):
+        raise ValueError("add_gate and add_up must be given together")
+    if add_gate is not None:
+        ag, au, ald = _pair(add_gate, add_up, ("add_gate", "add_up"), dw_gate, (N, K))
+        used = (dgate, dup, x, dw_gate, dw_up, add_gate, add_up)
+        if ald != wld and N > 1:
+            raise ValueError(f"add_gate has row stride {ald}, dw_gate {wld}")
+    _q8_call(_lib.zs_glu_weight_grad, "zs_glu_weight_grad", used,
+             (dgp, dupp, dld, xp, xld, fmt, T, N, K, ag, au, gp, upp, wfmt, wld), stream)
 
 
 # ------------------------------------------------------------ optimizer offload

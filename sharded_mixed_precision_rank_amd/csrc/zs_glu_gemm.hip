@@ -1,0 +1,564 @@
+// The products of the gated feed-forward block.
+//
+//   kForward  h = act(x Wg^T) * (x Wu^T)          both projections in one kernel, gate and up kept where asked for
+//   kInput    dx = dgate Wg + dup Wu              one sum over both
+//   kWeight   dWg = dgate^T x, dWu = dup^T x      (+ earlier micro-batches' sums), two products in one launch
+//
+// Operands are bf16 or fp16, sums fp32, each output rounded once.
+#include "zs_act.h"
+#include "zs_glu.h"
+#include "zs_tile_dev.h"
+
+namespace zs {
+namespace {
+
+using namespace dev;
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// c[r] += sum over 32 k of b's row 4 g + r and a's row i16, of two 16 x 32
+// fragments: lane (g, i16) holds row i16, k = 8 g .. 8 g + 7 of each.
+template <int FMT>
+__device__ __forceinline__ f32x4 mfma16(i32x4 b, i32x4 a, f32x4 c) {
+  if constexpr (FMT == kBF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
+}
+
+// RUN (4 or 8) results from element i on, of which the first `left` exist, plus
+// what add holds there.  PAST: around the caches, for 16-bit formats.
+template <int FMT, int RUN, bool PAST>
+__device__ __forceinline__ void store_run_as(void* d, const void* add, int64_t i, int64_t left, const float* x) {
+  float v[RUN];
+#pragma unroll
+  for (int r = 0; r < RUN; ++r) v[r] = x[r];
+  if (left >= RUN) {
+    if (add != nullptr) {
+#pragma unroll
+      for (int r = 0; r < RUN; r += 4) {
+        if constexpr (FMT == kFP32) {
+          const f32x4 w = ld_any<f32x4>((const float*)add + i + r);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[r + k] = w[k] + v[r + k];
+        } else {
+          const u32x2 w = ld_any<u32x2>((const uint16_t*)add + i + r);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[r + k] = (k % 2 ? h_hi<FMT>(w[k / 2]) : h_lo<FMT>(w[k / 2])) + v[r + k];
+        }
+      }
+    }
+    if constexpr (FMT == kFP32) {
+#pragma unroll
+      for (int r = 0; r < RUN; r += 4) st_four<FMT>(d, i + r, v + r);
+    } else if constexpr (RUN == 8) {
+      const u32x4 w = {pack_two<FMT>(v[0], v[1]), pack_two<FMT>(v[2], v[3]), pack_two<FMT>(v[4], v[5]),
+                       pack_two<FMT>(v[6], v[7])};
+      if constexpr (PAST)
+        st_past((uint16_t*)d + i, w);
+      else
+        st_any((uint16_t*)d + i, w);
+    } else {
+      st_four<FMT>(d, i, v);
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < RUN; ++r) {
+      if (r < left) st_elem<FMT>(d, i + r, add != nullptr ? ld_elem<FMT>(add, i + r) + v[r] : v[r]);
+    }
+  }
+}
+// The same in the weight gradient's output format, which need not be the operands'.
+template <int FMT, int RUN>
+__device__ __forceinline__ void store_grad(const GluGemm& a, int p, int64_t i, int64_t left, const float* v) {
+  if (a.out_format == ZS_FORMAT_FP32)
+    store_run_as<kFP32, RUN, false>(a.out[p], a.add[p], i, left, v);
+  else if (a.out_format == ZS_FORMAT_BF16)
+    store_run_as<kBF16, RUN, false>(a.out[p], a.add[p], i, left, v);
+  else
+    store_run_as<kFP16, RUN, false>(a.out[p], a.add[p], i, left, v);
+}
+// h, and gate and up where they are kept, at row m from column n on.
+template <int FMT, int RUN, bool PAST>
+__device__ __forceinline__ void store_gated(const GluGemm& a, int64_t m, int64_t n, const float* gate, const float* up) {
+  if (m >= a.M || n >= a.N) return;
+  float h[RUN], none;
+  switch (a.act) {
+    case ZS_ACT_SILU:
+#pragma unroll
+      for (int r = 0; r < RUN; ++r) h[r] = act_of<ZS_ACT_SILU, false>(gate[r], none) * up[r];
+      break;
+    case ZS_ACT_GELU:
+#pragma unroll
+      for (int r = 0; r < RUN; ++r) h[r] = act_of<ZS_ACT_GELU, false>(gate[r], none) * up[r];
+      break;
+    case ZS_ACT_GELU_TANH:
+#pragma unroll
+      for (int r = 0; r < RUN; ++r) h[r] = act_of<ZS_ACT_GELU_TANH, false>(gate[r], none) * up[r];
+      break;
+    default:
+#pragma unroll
+      for (int r = 0; r < RUN; ++r) h[r] = act_of<ZS_ACT_RELU, false>(gate[r], none) * up[r];
+  }
+  store_run_as<FMT, RUN, PAST>(a.out[0], nullptr, m * a.ldo[0] + n, a.N - n, h);
+  if (a.out[1] != nullptr) {
+    store_run_as<FMT, RUN, PAST>(a.out[1], nullptr, m * a.ldo[1] + n, a.N - n, gate);
+    store_run_as<FMT, RUN, PAST>(a.out[2], nullptr, m * a.ldo[2] + n, a.N - n, up);
+  }
+}
+
+// Values of a fragment's dwords past the end of the summed axis: `left` of the lane's 8 are inside.
+__device__ __forceinline__ i32x4 inside(int left) {
+  i32x4 mask;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const int n = left - 2 * d;
+    mask[d] = n >= 2 ? -1 : n == 1 ? 0xFFFF : 0;
+  }
+  return mask;
+}
+
+// ---------------------------------------------------------------------------
+// Rows at any address: 64 x 64 sums per workgroup of four waves (32 x 32 each),
+// operands staged through registers 16 bytes at a time, 64 of the summed axis a
+// step.  Forward: 32 columns of gate beside the same 32 of up.
+// ---------------------------------------------------------------------------
+constexpr int kAnyTile = 64;
+constexpr int kStage = 64;  // of the summed axis a stage: 128 bytes of a row
+
+template <GluOp OP, int FMT>
+__global__ __launch_bounds__(256) void glu_any(const GluGemm a, int64_t tiles_n, int64_t tiles) {
+  constexpr bool kARow = OP != GluOp::kWeight, kBRow = OP == GluOp::kForward;
+  constexpr int kOutN = OP == GluOp::kForward ? 32 : 64;
+  __shared__ __attribute__((aligned(16))) char lds_a[8192];
+  __shared__ __attribute__((aligned(16))) char lds_b[8192];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
+  const int g = lane >> 4, i16 = lane & 15;
+  constexpr int kParts = OP == GluOp::kForward ? 1 : 2;  // kInput: summed; kWeight: side by side
+  const int64_t all = OP == GluOp::kWeight ? 2 * tiles : tiles;
+  for (int64_t at = blockIdx.x; at < all; at += gridDim.x) {
+    const int out = at >= tiles ? 1 : 0;
+    const int64_t tile = at - out * tiles;
+    const int64_t m0 = tile / tiles_n * kAnyTile, n0 = tile % tiles_n * kOutN;
+    f32x4 acc[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
+    for (int part = 0; part < (OP == GluOp::kInput ? kParts : 1); ++part) {
+      const int pa = OP == GluOp::kInput ? part : out;
+      const char* pa_base = (const char*)a.a[OP == GluOp::kForward ? 0 : pa];
+      const char* pb_base = (const char*)a.b[OP == GluOp::kInput ? part : 0];
+      for (int64_t k0 = 0; k0 < a.K; k0 += kStage) {
+        u32x4 ra[2], rb[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int p = tid + 256 * c, row = p / 8, col = p % 8 * 16;  // 8 pieces a row of 64 values
+          if constexpr (kARow) {
+            const int64_t m = m0 + row;
+            ra[c] = ld_piece<2>(pa_base + m * a.lda * 2, k0 * 2 + col, a.K * 2, m < a.M);
+          } else {
+            const int64_t k = k0 + row;
+            ra[c] = ld_piece<2>(pa_base + k * a.lda * 2, m0 * 2 + col, a.M * 2, k < a.K);
+          }
+          if constexpr (kBRow) {  // rows 0 .. 31 of gate, then of up
+            const int64_t n = n0 + row % 32;
+            rb[c] = ld_piece<2>((const char*)a.b[row / 32] + n * a.ldb * 2, k0 * 2 + col, a.K * 2, n < a.N);
+          } else {
+            const int64_t k = k0 + row;
+            rb[c] = ld_piece<2>(pb_base + k * a.ldb * 2, n0 * 2 + col, a.N * 2, k < a.K);
+          }
+        }
+        __syncthreads();  // the step before has been read
+        auto place = [](int row, int piece, bool by_row) {
+          return row * 128 + (piece ^ (by_row ? row & 7 : (row & 3) << 1)) * 16;
+        };
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int p = tid + 256 * c;
+          *(u32x4*)(lds_a + place(p / 8, p % 8, kARow)) = ra[c];
+          *(u32x4*)(lds_b + place(p / 8, p % 8, kBRow)) = rb[c];
+        }
+        __syncthreads();
+        auto by_row = [&](const char* base, int r, int half) {
+          return *(const i32x4*)(base + r * 128 + ((4 * half + g) ^ (r & 7)) * 16);
+        };
+        auto turned = [&](const char* base, int col, int half) {  // 8 rows of the summed axis x 16 columns
+          const int row = 32 * half + 8 * g + (i16 >> 2);
+          const char* q = base + row * 128 + ((col / 8 + (i16 >> 1 & 1)) ^ (row & 3) << 1) * 16 + (i16 & 1) * 8;
+          const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)q);
+          const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(q + 4 * 128));
+          return __builtin_bit_cast(i32x4, (i16x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+        };
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          i32x4 fa[2], fb[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if constexpr (kARow)
+              fa[i] = by_row(lds_a, wm + i * 16 + i16, half);
+            else
+              fa[i] = turned(lds_a, wm + i * 16, half);
+            if constexpr (kBRow)  // 16 columns of gate, then of up
+              fb[i] = by_row(lds_b, i * 32 + wn / 2 + i16, half);
+            else
+              fb[i] = turned(lds_b, wn + i * 16, half);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[i][j] = mfma16<FMT>(fb[j], fa[i], acc[i][j]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t m = m0 + wm + i * 16 + i16;
+      if constexpr (OP == GluOp::kForward) {
+        float gate[4], up[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) gate[r] = acc[i][0][r], up[r] = acc[i][1][r];
+        store_gated<FMT, 4, false>(a, m, n0 + wn / 2 + 4 * g, gate, up);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int64_t n = n0 + wn + j * 16 + 4 * g;
+          if (m >= a.M || n >= a.N) continue;
+          float v[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = acc[i][j][r];
+          if constexpr (OP == GluOp::kInput)
+            store_run_as<FMT, 4, false>(a.out[0], nullptr, m * a.ldo[0] + n, a.N - n, v);
+          else
+            store_grad<FMT, 4>(a, out, m * a.ldo[out] + n, a.N - n, v);
+        }
+      }
+    }
+    __syncthreads();  // before the next tile's first pieces are written
+  }
+}
+
+template <GluOp OP, int FMT>
+hipError_t any_launch(const GluGemm& a, hipStream_t stream) {
+  const int64_t tm = (a.M + kAnyTile - 1) / kAnyTile;
+  const int64_t wide = OP == GluOp::kForward ? 32 : 64, tn = (a.N + wide - 1) / wide;
+  const int64_t tiles = tm * tn, all = OP == GluOp::kWeight ? 2 * tiles : tiles;
+  const dim3 grid((unsigned)(all < (1 << 20) ? all : (1 << 20)));
+  glu_any<OP, FMT><<<grid, 256, 0, stream>>>(a, tn, tiles);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Rows on 16-byte boundaries: BM x BN sums per workgroup of WM x WN waves,
+// pieces of both operands moved from memory into LDS directly, 64 of the summed
+// axis a stage and NS stages in a ring.  A wave holds its fragments of the next
+// 32 in registers while the matrix instructions take the current ones, so that
+// LDS reads, memory loads and matrix instructions run side by side.  One barrier
+// a stage: between its halves every wave has read all of the stage and its part
+// of the next one has landed.
+//
+// An operand whose rows run along the summed axis lies in rows of 128 bytes,
+// read 16 bytes a lane; one whose rows lie across it (both weights in kInput,
+// everything in kWeight) lies as in memory and is turned by the transposing LDS
+// reads.  Forward: b's tile holds, for each wave's 64 columns, 32 rows of gate and
+// the same 32 of up, so that a lane ends with 8 columns of both.
+// ---------------------------------------------------------------------------
+template <GluOp OP, int FMT, int BM, int BN, int WM, int WN, int NS, bool PAST>
+__global__ __launch_bounds__(WM* WN * 64, 2) void glu_tile(const GluGemm a, uint32_t tiles_m, uint32_t tiles_n) {
+  constexpr bool kForward = OP == GluOp::kForward, kInput = OP == GluOp::kInput, kWeight = OP == GluOp::kWeight;
+  constexpr bool kARow = !kWeight, kBRow = kForward;
+  constexpr int kWaves = WM * WN, kOutN = kForward ? BN / 2 : BN;
+  constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  // across the summed axis: 8 rows, and 128 bytes that put the next 8 in the other half of the banks
+  constexpr int kAGroup = 8 * BM * 2 + 128, kBGroup = 8 * BN * 2 + 128;
+  constexpr int kABytes = kARow ? BM * 128 : 8 * kAGroup, kBBytes = kBRow ? BN * 128 : 8 * kBGroup;
+  constexpr int kBuf = kABytes + kBBytes;
+  constexpr int kALoads = BM / 8 / kWaves, kBLoads = BN / 8 / kWaves;
+  static_assert(FN % 2 == 0 && kALoads > 0 && kBLoads > 0 && (NS & (NS - 1)) == 0 && (!kForward || (TN == 64 && kBLoads <= 4)),
+                "tile shape");
+  __shared__ __attribute__((aligned(1024))) char lds[NS * kBuf];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, i16 = lane & 15;
+  const int wm = wave / WN * TM, wn = wave % WN * TN;
+  const int out = kWeight ? (int)blockIdx.y : 0;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * kOutN;
+  const int32_t K = (int32_t)a.K;
+  const int nk = (int)(((int64_t)K + kStage - 1) / kStage), stages = kInput ? 2 * nk : nk;
+  const int32_t pitch_a = (int32_t)a.lda * 2, pitch_b = (int32_t)a.ldb * 2;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS char*)lds;
+  const char* const a0 = (const char*)a.a[kWeight ? out : 0];
+  const char* const b0 = (const char*)a.b[0];
+  // kInput: the second half of the stages are of the second pair of operands
+  auto a_of = [&](int stage) { return kInput && stage >= nk ? (const char*)a.a[1] : a0; };
+  auto b_of = [&](int stage) { return kInput && stage >= nk ? (const char*)a.b[1] : b0; };
+  auto k_of = [&](int stage) { return (int64_t)(kInput && stage >= nk ? stage - nk : stage) * kStage; };
+  // rows of the summed axis that a stage has (none past the last stage)
+  auto rows_at = [&](int stage) {
+    if (stage >= stages) return 0;
+    const int64_t left = K - k_of(stage);
+    return (int)(left < kStage ? left : kStage);
+  };
+
+  // Along the summed axis: piece c of row r lies at place c ^ s(r), s = the lane's row in a fragment & 7, so that the 8
+  // lanes that read one bank width at a time read 8 different places.  b's fragment rows i16 are columns
+  // (i16 / 4) * 8 + 4 (j % 2) + i16 % 4 of the 32 of two fragments, which leaves each lane 8 consecutive columns.
+  const int32_t rows_a = left_of(a.M, m0, BM), cols_b = left_of(a.N, n0, kOutN);
+  const uint32_t va_row = (uint32_t)(lane >> 3) * (uint32_t)pitch_a + (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);
+  uint32_t vb_row[2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+    vb_row[p] = (uint32_t)(lane >> 3) * (uint32_t)pitch_b + (uint32_t)(((lane & 7) ^ ((lane >> 3 & 3) | p << 2)) * 16);
+  // A stage past the last lies past the end of every buffer: zeros, and no traffic.
+  auto from = [&](int stage) { return stage < stages ? (uint32_t)(k_of(stage) * 2) : 0x7FFFFFF0u; };
+  // Across it: piece c of row r at place c ^ s(r).  A transposing read takes 32 bytes of 4 consecutive rows, and of 4
+  // that lie 8 rows on, per 32 lanes: s puts those 4 at different places.
+  auto s_of = [](int row) { return (row & 3) << 1; };
+  constexpr int kAPer = BM / 8, kBPer = BN / 8;            // pieces in a row
+  constexpr int kARows = 64 / kAPer, kBRows = 64 / kBPer;  // rows a load
+  constexpr int kAApart = kARows >= 4 ? 1 : 4 / kARows, kBApart = kBRows >= 4 ? 1 : 4 / kBRows;  // loads to the same s
+  uint32_t va_col[kAApart], vb_col[kBApart];
+#pragma unroll
+  for (int j = 0; j < kAApart; ++j) {
+    const int row = (wave * kALoads + j) * kARows + lane / kAPer;
+    va_col[j] = (uint32_t)row * (uint32_t)pitch_a + (uint32_t)(((lane % kAPer) ^ s_of(row)) * 16);
+  }
+#pragma unroll
+  for (int j = 0; j < kBApart; ++j) {
+    const int row = (wave * kBLoads + j) * kBRows + lane / kBPer;
+    vb_col[j] = (uint32_t)row * (uint32_t)pitch_b + (uint32_t)(((lane % kBPer) ^ s_of(row)) * 16);
+  }
+
+  // Forward: this wave's loads of b are all of gate or all of up.
+  const int up = kForward ? wave * kBLoads / 4 % 2 : 0;
+  const Rsrc rb_row = make_rsrc((const char*)a.b[up] + n0 * a.ldb * 2, cols_b, K * 2, pitch_b);
+  auto load_a = [&](int stage, int j) {
+    const int t = wave * kALoads + j;
+    const uint32_t to = lds0 + (stage & (NS - 1)) * kBuf;
+    if constexpr (kARow) {
+      const Rsrc r = make_rsrc(a_of(stage) + m0 * a.lda * 2, rows_a, K * 2, pitch_a);
+      load_to_lds(r, va_row + (uint32_t)(t * 8) * (uint32_t)pitch_a + from(stage), to + t * 1024);
+    } else {
+      const Rsrc r = make_rsrc(a_of(stage) + (k_of(stage) * a.lda + m0) * 2, rows_at(stage), rows_a * 2, pitch_a);
+      load_to_lds(r, va_col[j % kAApart] + (uint32_t)(j / kAApart * kAApart * kARows) * (uint32_t)pitch_a,
+                  to + t * kARows / 8 * kAGroup + t * kARows % 8 * BM * 2);
+    }
+  };
+  auto load_b = [&](int stage, int j) {
+    const int t = wave * kBLoads + j;
+    const uint32_t to = lds0 + (stage & (NS - 1)) * kBuf + kABytes;
+    if constexpr (kBRow) {
+      const int row = t / 8 * 32 + t % 4 * 8;  // of gate or up
+      load_to_lds(rb_row, vb_row[t & 1] + (uint32_t)row * (uint32_t)pitch_b + from(stage), to + t * 1024);
+    } else {
+      const Rsrc r = make_rsrc(b_of(stage) + (k_of(stage) * a.ldb + n0) * 2, rows_at(stage), cols_b * 2, pitch_b);
+      load_to_lds(r, vb_col[j % kBApart] + (uint32_t)(j / kBApart * kBApart * kBRows) * (uint32_t)pitch_b,
+                  to + t * kBRows / 8 * kBGroup + t * kBRows % 8 * BN * 2);
+    }
+  };
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
+  i32x4 fa[2][FM], fb[2][FN];
+
+  const int s7 = i16 & 7;
+  const int at_a_row = (wm + i16) * 128;
+  const int at_b_row = kABytes + (wn + (i16 >> 2) * 8 + (i16 & 3)) * 128;
+  // A lane's place in the rows of a transposing read of 16 columns from 16 c on.
+  auto place_of = [&](int group, int pitch, int c) {
+    return (uint32_t)(g * group + (i16 >> 2) * pitch + ((2 * (c & 3) + (i16 >> 1 & 1)) ^ (i16 >> 2) << 1) * 16 + (i16 & 1) * 8 +
+                      (c >> 2) * 128);
+  };
+  constexpr int kAPlaces = FM < 4 ? FM : 4, kBPlaces = FN < 4 ? FN : 4;
+  static_assert((FM <= 4 || TM % 64 == 0) && (FN <= 4 || TN % 64 == 0), "places repeat");
+  uint32_t place_a[kAPlaces], place_b[kBPlaces];
+#pragma unroll
+  for (int v = 0; v < kAPlaces; ++v) place_a[v] = place_of(kAGroup, BM * 2, (wm >> 4) + v);
+#pragma unroll
+  for (int v = 0; v < kBPlaces; ++v) place_b[v] = kABytes + place_of(kBGroup, BN * 2, (wn >> 4) + v);
+  auto turned = [&](uint32_t at, int pitch4) {  // 8 rows (4 and 4)
+    LDS char* p = (LDS char*)lds + at;
+    const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)p);
+    const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(p + pitch4));
+    return __builtin_bit_cast(i32x4, (i16x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+  };
+  auto read_a = [&](int buf, int half, int i) {
+    if constexpr (kARow)
+      fa[half][i] = *(const LDS i32x4*)((LDS char*)lds + buf * kBuf + at_a_row + i * 16 * 128 + ((4 * half + g) ^ s7) * 16);
+    else
+      fa[half][i] = turned(place_a[i % kAPlaces] + (uint32_t)(buf * kBuf + half * 4 * kAGroup + i / 4 * 128), 4 * BM * 2);
+  };
+  auto read_b = [&](int buf, int half, int j) {
+    if constexpr (kBRow)
+      fb[half][j] = *(const LDS i32x4*)((LDS char*)lds + buf * kBuf + at_b_row + (j / 2 * 32 + j % 2 * 4) * 128 +
+                                        ((4 * half + g) ^ s7) * 16);
+    else
+      fb[half][j] = turned(place_b[j % kBPlaces] + (uint32_t)(buf * kBuf + half * 4 * kBGroup + j / 4 * 128), 4 * BN * 2);
+  };
+  // The last stage's values past K are whatever the rows go on with: zero them (in both operands, for they may not be
+  // finite).  Rows across the summed axis are read as zeros past its end.
+  auto cut = [&](int stage, int half) {
+    if constexpr (kARow) {
+      if (K % kStage != 0 && (stage == stages - 1 || (kInput && stage == nk - 1))) {
+        const i32x4 mask = inside(K - (nk - 1) * kStage - half * 32 - 8 * g);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) fa[half][i] &= mask;
+        if constexpr (kBRow) {
+#pragma unroll
+          for (int j = 0; j < FN; ++j) fb[half][j] &= mask;
+        }
+      }
+    }
+  };
+  // The matrix instructions of one half of a stage, with the fragment reads of the next half and, in the second, the
+  // memory loads of stage `stage` + NS (into the buffer of the present one) spread between them.
+  constexpr int kLoads = kALoads + kBLoads, kMfma = FM * FN;
+  auto half_step = [&](auto half_c, int stage) {
+    constexpr int half = decltype(half_c)::value;
+    const int buf_next = (stage + half) & (NS - 1);
+    cut(stage, half);
+    for_each<kMfma>([&](auto at_c) {
+      constexpr int at = decltype(at_c)::value, i = at / FN, j = at % FN;
+      // the next fragments of a as the present ones come to their last use, those of b in the first half
+      if constexpr (j == 0) read_a(buf_next, half ^ 1, i);
+      for_each<FN>([&](auto r) {
+        if constexpr (r >= at * 2 * FN / kMfma && r < (at + 1) * 2 * FN / kMfma) read_b(buf_next, half ^ 1, r);
+      });
+      acc[i][j] = mfma16<FMT>(fb[half][j], fa[half][i], acc[i][j]);
+      if constexpr (half == 1) {
+        for_each<kLoads>([&](auto l) {
+          if constexpr (l >= at * kLoads / kMfma && l < (at + 1) * kLoads / kMfma) {
+            if constexpr (l < kALoads)
+              load_a(stage + NS, l);
+            else
+              load_b(stage + NS, l - kALoads);
+          }
+        });
+      }
+      if constexpr (at % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  // The ring: stage s lies in buffer s % NS; stage s + NS is loaded into it once every wave has read the last of s.
+  if (stages > 0) {
+#pragma unroll
+    for (int p = 0; p < NS; ++p) {
+#pragma unroll
+      for (int j = 0; j < kALoads; ++j) load_a(p, j);
+#pragma unroll
+      for (int j = 0; j < kBLoads; ++j) load_b(p, j);
+    }
+    meet<(NS - 1) * kLoads>();
+#pragma unroll
+    for (int j = 0; j < FN; ++j) read_b(0, 0, j);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) read_a(0, 0, i);
+    for (int s = 0; s < stages; ++s) {
+      half_step(First{}, s);
+      meet<(NS - 2) * kLoads>();  // all but the stages after the next have landed
+      half_step(Second{}, s);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way to LDS when the workgroup ends
+  }
+
+  // Results: lane i16 holds row i16 of a fragment, 8 consecutive columns from two accumulators (after a trade where b
+  // was turned), so that a store covers 64 bytes of each of 16 rows.
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = m0 + wm + i * 16 + i16;
+    if constexpr (kForward) {
+      float v[2][8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) v[0][r] = acc[i][r / 4][r % 4], v[1][r] = acc[i][2 + r / 4][r % 4];
+      store_gated<FMT, 8, PAST>(a, m, n0 + wn / 2 + g * 8, v[0], v[1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < FN; j += 2) {
+        float v[8];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          uint32_t lo, hi;
+          trade(__float_as_uint(acc[i][j][r]), __float_as_uint(acc[i][j + 1][r]), lo, hi);
+          v[r] = __uint_as_float(lo);
+          v[4 + r] = __uint_as_float(hi);
+        }
+        const int64_t n = n0 + wn + j * 16 + eight_at(g);
+        if (m >= a.M || n >= a.N) continue;
+        if constexpr (kInput)
+          store_run_as<FMT, 8, PAST>(a.out[0], nullptr, m * a.ldo[0] + n, a.N - n, v);
+        else
+          store_grad<FMT, 8>(a, out, m * a.ldo[out] + n, a.N - n, v);
+      }
+    }
+  }
+}
+
+template <GluOp OP, int FMT, int BM, int BN, int WM, int WN, int NS>
+hipError_t tile_launch(const GluGemm& a, hipStream_t stream) {
+  constexpr int kOutN = OP == GluOp::kForward ? BN / 2 : BN;
+  const uint32_t tm = (uint32_t)((a.M + BM - 1) / BM), tn = (uint32_t)((a.N + kOutN - 1) / kOutN);
+  const dim3 grid(tm * tn, OP == GluOp::kWeight ? 2 : 1);
+  if constexpr (BM >= 128 && OP != GluOp::kWeight) {
+    bool whole = true;  // 16-bit outputs in whole pieces of 64 bytes
+    for (int p = 0; p < 3; ++p) whole = whole && (a.out[p] == nullptr || ((uintptr_t)a.out[p] | (uintptr_t)(a.ldo[p] * 2)) % 64 == 0);
+    if (whole) {
+      glu_tile<OP, FMT, BM, BN, WM, WN, NS, true><<<grid, WM * WN * 64, 0, stream>>>(a, tm, tn);
+      return hipGetLastError();
+    }
+  }
+  glu_tile<OP, FMT, BM, BN, WM, WN, NS, false><<<grid, WM * WN * 64, 0, stream>>>(a, tm, tn);
+  return hipGetLastError();
+}
+
+// Rows that the tiled kernels take: on 16-byte boundaries (a single row at any
+// distance from the next), offsets within a tile below 2^31, a grid that a
+// launch can hold.
+bool rows16(const void* p, int64_t rows, int64_t ld) {
+  return (uintptr_t)p % 16 == 0 && (rows <= 1 || (ld % 8 == 0 && ld <= (1 << 21)));
+}
+int64_t tiles_of(const GluGemm& a, int64_t bm, int64_t bn) { return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn); }
+constexpr int64_t kMostTiles = 1 << 22;
+
+template <GluOp OP, int FMT>
+hipError_t gemm_launch(const GluGemm& given, hipStream_t stream) {
+  GluGemm a = given;
+  const bool weight = OP == GluOp::kWeight, forward = OP == GluOp::kForward;
+  const int64_t rows_a = weight ? a.K : a.M, rows_b = forward ? a.N : a.K;
+  bool fast = a.K > 0 && tiles_of(a, 64, 32) < kMostTiles && rows16(a.a[0], rows_a, a.lda) && rows16(a.b[0], rows_b, a.ldb);
+  if (!forward) fast = fast && rows16(a.a[1], rows_a, a.lda);
+  if (!weight) fast = fast && rows16(a.b[1], rows_b, a.ldb);
+  if (!weight) fast = fast && a.K <= (1 << 21);  // (a single row may be longer)
+  if (!fast) return any_launch<OP, FMT>(a, stream);
+  // a single row: any distance that holds what a tile reads of it
+  const int64_t wide_a = weight ? 256 : a.K, wide_b = forward ? a.K : 256;
+  if (rows_a <= 1) a.lda = (wide_a + 255) / 256 * 256;
+  if (rows_b <= 1) a.ldb = (wide_b + 255) / 256 * 256;
+  const int64_t parts = weight ? 2 : 1, half = forward ? 2 : 1;
+  const int64_t t256 = parts * tiles_of(a, 256, 256 / half), t128 = parts * tiles_of(a, 128, 128 / half),
+                t64 = parts * tiles_of(a, 64, 64 / half);
+  if (t64 <= 256) return tile_launch<OP, FMT, 64, 64, 4, 1, 4>(a, stream);
+  if (t128 <= 256) return tile_launch<OP, FMT, 128, 128, 4, 2, 4>(a, stream);
+  if (t256 <= 200) return tile_launch<OP, FMT, 128, 128, 2, 2, 2>(a, stream);
+  return tile_launch<OP, FMT, 256, 256, 2, 4, 2>(a, stream);
+}
+
+template <GluOp OP>
+hipError_t by_format(const GluGemm& a, hipStream_t stream) {
+  return a.format == ZS_FORMAT_BF16 ? gemm_launch<OP, kBF16>(a, stream) : gemm_launch<OP, kFP16>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_glu_gemm(GluOp op, const GluGemm& a, hipStream_t stream) {
+  switch (op) {
+    case GluOp::kForward: return by_format<GluOp::kForward>(a, stream);
+    case GluOp::kInput: return by_format<GluOp::kInput>(a, stream);
+    default: return by_format<GluOp::kWeight>(a, stream);
+  }
+}
+
+}  // namespace zs
