@@ -585,6 +585,85 @@ ZS_API zs_status zs_glu_weight_grad(const void* dgate, const void* dup, int64_t 
                                     const void* add_up, void* dw_gate, void* dw_up, int32_t dw_format, int64_t ld_dw,
                                     zs_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * Orthogonalised updates of weight matrices (the Muon optimiser's step).
+ *
+ * zs_reduce_muon is the matrix counterpart of zs_reduce_adam_flat: it takes the
+ * same N replicas of a weight's gradient and updates the same fp32 master and
+ * bf16 working copy, but with one momentum of state instead of two, and with an
+ * update whose singular values are all about 1:
+ *
+ *   reduce      g = mean of the replicas, as zs_reduce_adam_flat has it
+ *   momentum    M1 = mu*M + g;  U = g + mu*M1 (nesterov) or M1
+ *   orthogonal  O = the Newton-Schulz steps of U
+ *   update      p1 = dk*P - ss*O;  B = bf16_rne(p1)
+ *
+ * with mu = momentum, dk = 1 - lr*weight_decay, ss = lr*scale (folded in double,
+ * rounded once to fp32).  reduce, momentum and update are fp32, one rounding per
+ * operation in this order.  zs_orthogonalize is the third line on its own.
+ *
+ * The Newton-Schulz steps of a matrix U (rows x cols), with coefficients (a, b,
+ * c) for each step:
+ *
+ *   X = U / |U|_F;   X <- a X + (b S + c S^2) X with S = X X^T
+ *
+ * (rows <= cols; a matrix with more rows goes by its transpose, which is the
+ * same polynomial of its singular values).  The norm is summed in double; the
+ * products' operands are held in 22 bits (two fp16 parts), their sums in fp32:
+ * results are about as near to exact ones as plain fp32 products would be (1e-6
+ * of |X| for five default steps; the steps magnify roundings of directions with
+ * small singular values, by up to a each).  A matrix of zeros gives zeros; one
+ * with a NaN or an infinity gives NaN throughout, and nothing else in its batch
+ * changes.  Coefficients that take entries of X, S or b S + c S^2 past 15.9 end
+ * in NaN; those that keep singular values in [0, 1] below 1.5 stay within 4.
+ *
+ * Matrices of a batch are done side by side.  Sizes: batch 0 .. 65535, rows and
+ * cols 0 .. 2^20, the smaller of the two at most 2^16; nothing is written when
+ * one is 0.  Results are the same call to call, whatever runs beside it.
+ *
+ * Workspace: device memory of zs_orthogonalize_workspace_bytes, any alignment,
+ * whatever it holds; its contents mean nothing after the call.  Two calls whose
+ * kernels may run at the same time (two streams, two captured graphs) need one
+ * each.  Every call enqueues kernels on `stream` only and may be captured.
+ * ------------------------------------------------------------------------- */
+
+#define ZS_MUON_MAX_STEPS 32
+
+typedef struct zs_muon_hp {
+  double lr, momentum, weight_decay;
+  double scale;        /* of the update beside lr, e.g. 0.2 sqrt(max(rows, cols)) */
+  int32_t nesterov;    /* 0 or 1 */
+  int32_t steps;       /* 1 .. ZS_MUON_MAX_STEPS */
+  const double* coefs; /* host: (a, b, c) of each step, 3 * steps values; NULL: 3.4445, -4.7750, 2.0315 for each */
+} zs_muon_hp;
+
+/* Bytes of workspace for these sizes (0 for an empty batch, and for sizes past
+   the limits).  About 8 bytes a value and 8 a value of the smaller square. */
+ZS_API size_t zs_orthogonalize_workspace_bytes(int64_t rows, int64_t cols, int64_t batch);
+
+/* out = the Newton-Schulz steps of x, for each matrix of a batch.  x in x_format,
+   out in out_format (BF16, FP16 or FP32): row-major, ld elements from row to row
+   and batch_stride elements from matrix to matrix, at least rows * ld (neither is
+   looked at where there is one).  Any alignment of the elements.  coefs as in
+   zs_muon_hp.  out may be x itself (same format, ld and batch stride).
+   Errors: ZS_ERR_NULL, ZS_ERR_RANGE (also: workspace too small; coefficients not
+   finite), ZS_ERR_ALIGN, ZS_ERR_ALIAS, ZS_ERR_HIP. */
+ZS_API zs_status zs_orthogonalize(const void* x, int32_t x_format, int64_t ld_x, int64_t batch_stride_x, int64_t batch,
+                                  int64_t rows, int64_t cols, int32_t steps, const double* coefs, void* out,
+                                  int32_t out_format, int64_t ld_out, int64_t batch_stride_out, void* workspace,
+                                  size_t workspace_bytes, zs_stream stream);
+
+/* The step of a batch of matrices, contiguous one behind the other in every
+   array (a run of equal layers in a flat shard): batch * rows * cols values.
+   grad_chunks: N bf16 arrays, 1 <= N <= ZS_MAX_REPLICAS (the host array is read
+   during the call).  Any alignment of the elements.  master, momentum and
+   param_bf16 are updated; no array may overlap another one.
+   Errors as zs_orthogonalize (hyperparameters not finite, lr, momentum or
+   weight_decay below 0, momentum 1 or more: ZS_ERR_RANGE). */
+ZS_API zs_status zs_reduce_muon(const uint16_t* const* grad_chunks, int32_t N, int64_t batch, int64_t rows, int64_t cols,
+                                float* master, float* momentum, uint16_t* param_bf16, const zs_muon_hp* hp,
+                                void* workspace, size_t workspace_bytes, zs_stream stream);
+
 /* Workgroups per launch for all later step calls in this process: 0 picks
    automatically from the device's compute-unit count.  Results do not depend
    on it (every element is computed by one thread with the same operations). */

@@ -168,6 +168,21 @@ _lib.zs_glu_weight_grad.argtypes = [_vp, _vp, _i64, _vp, _i64, _i32, _i64, _i64,
                                     _vp]
 
 
+class MuonHPStruct(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("scale", ctypes.c_double), ("nesterov", _i32), ("steps", _i32), ("coefs", ctypes.POINTER(ctypes.c_double))]
+
+
+_lib.zs_orthogonalize_workspace_bytes.restype = ctypes.c_size_t
+_lib.zs_orthogonalize_workspace_bytes.argtypes = [_i64, _i64, _i64]
+_lib.zs_orthogonalize.restype = ctypes.c_int
+_lib.zs_orthogonalize.argtypes = [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _i32, ctypes.POINTER(ctypes.c_double), _vp, _i32,
+                                  _i64, _i64, _vp, ctypes.c_size_t, _vp]
+_lib.zs_reduce_muon.restype = ctypes.c_int
+_lib.zs_reduce_muon.argtypes = [ctypes.POINTER(_vp), _i32, _i64, _i64, _i64, _vp, _vp, _vp, ctypes.POINTER(MuonHPStruct), _vp,
+                                ctypes.c_size_t, _vp]
+
+
 FORMATS = {"bf16": 0, "fp16": 1}
 Q8_SCALES = {"amax": 0, "pow2": 1}
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
@@ -1046,6 +1061,104 @@ def glu_weight_grad(dgate, dup, x, dw_gate, dw_up, add_gate=None, add_up=None, s
             raise ValueError(f"add_gate has row stride {ald}, dw_gate {wld}")
     _q8_call(_lib.zs_glu_weight_grad, "zs_glu_weight_grad", used,
              (dgp, dupp, dld, xp, xld, fmt, T, N, K, ag, au, gp, upp, wfmt, wld), stream)
+
+
+# ------------------------------------------------------------ orthogonalised updates
+def orthogonalize_workspace_bytes(rows: int, cols: int, batch: int = 1) -> int:
+    return int(_lib.zs_orthogonalize_workspace_bytes(rows, cols, batch))
+
+
+def _coefs(coefs, steps):
+    """(a, b, c) for each step as a C array: None (the defaults), one triple for all, or a sequence of ``steps``."""
+    if coefs is None:
+        return None
+    coefs = list(coefs)
+    if coefs and not hasattr(coefs[0], "__len__"):
+        coefs = [coefs] * steps
+    if len(coefs) != steps or any(len(c) != 3 for c in coefs):
+        raise ValueError(f"coefs must be one (a, b, c), or one for each of the {steps} steps")
+    return (ctypes.c_double * (3 * steps))(*[v for c in coefs for v in c])
+
+
+@dataclass(frozen=True)
+class MuonHP:
+    """``scale`` multiplies the update beside ``lr``; ``coefs``: None, one (a, b, c), or one for each step."""
+    lr: float = 1e-3
+    momentum: float = 0.95
+    weight_decay: float = 0.0
+    scale: float = 1.0
+    nesterov: bool = True
+    steps: int = 5
+    coefs: Optional[Sequence] = None
+
+    def _c(self) -> MuonHPStruct:
+        return MuonHPStruct(self.lr, self.momentum, self.weight_decay, self.scale, int(self.nesterov), self.steps,
+                            _coefs(self.coefs, self.steps))
+
+
+def _ns_workspace(workspace, rows, cols, batch, device, stream):
+    """The caller's workspace, or one of this call's own, whose reuse waits for ``stream``."""
+    if workspace is not None:
+        _dev_check(workspace, _WORKSPACE_TYPES, "workspace")
+        return workspace, workspace.numel() * workspace.element_size()
+    n = orthogonalize_workspace_bytes(rows, cols, batch)
+    workspace = torch.empty(n, dtype=torch.uint8, device=device)
+    if stream is not None:
+        workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                torch.cuda.ExternalStream(stream, device=device))
+    return workspace, n
+
+
+def _batched(t, formats, name):
+    """(address, batch, rows, columns, row stride, batch stride, format) of a matrix or a stack of them."""
+    if isinstance(t, torch.Tensor) and t.dim() == 3 and t.dtype in formats:
+        batch, rows, cols = t.shape
+        each, ld, step = t.stride()
+        if step != 1 and cols > 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        return t.data_ptr(), batch, rows, cols, ld, each, formats[t.dtype]
+    p, rows, cols, ld, fmt = _matrix(t, formats, name)
+    return p, 1, rows, cols, ld, 0, fmt
+
+
+def orthogonalize(x, out, workspace=None, steps: int = 5, coefs=None, stream=None) -> None:
+    """``out`` = the Newton-Schulz steps of ``x``: a matrix, or a stack of them (batch x rows x cols), in bf16, fp16 or
+    fp32 each.  ``coefs``: None, one (a, b, c), or one for each step.  ``workspace``: device memory of
+    :func:`orthogonalize_workspace_bytes`, or None to allocate it; see zs_orthogonalize."""
+    xp, batch, rows, cols, xld, xb, xf = _batched(x, _Q8_FORMATS, "x")
+    op, ob, orows, ocols, old, obs, of = _batched(out, _Q8_FORMATS, "out")
+    if (ob, orows, ocols) != (batch, rows, cols):
+        raise ValueError(f"out is {tuple(out.shape)}, x {tuple(x.shape)}")
+    c = _coefs(coefs, steps)
+    if not x.is_cuda or not out.is_cuda:
+        raise ValueError("zs_orthogonalize: every array must be a device tensor")
+    ws, ws_bytes = _ns_workspace(workspace, rows, cols, batch, x.device, stream)
+    _q8_call(_lib.zs_orthogonalize, "zs_orthogonalize", (x, out, ws),
+             (xp, xf, xld, xb, batch, rows, cols, steps, c, op, of, old, obs, ws.data_ptr(), ws_bytes), stream)
+
+
+def reduce_muon(grads: Sequence, master, momentum, param, hp, workspace=None, stream=None) -> None:
+    """One step of a weight matrix, or of a stack of them (batch x rows x cols), by an orthogonalised update: average
+    ``grads`` (bf16 tensors of ``master``'s shape), update ``momentum``, ``master`` (fp32) and ``param`` (bf16).  ``hp``: a
+    :class:`MuonHP` or a dict of its fields; see zs_reduce_muon."""
+    _dev_check(master, _F32, "master")
+    if master.dim() not in (2, 3):
+        raise ValueError(f"master must be a matrix or a stack of them, not of {master.dim()} dimensions")
+    batch = master.shape[0] if master.dim() == 3 else 1
+    rows, cols = master.shape[-2:]
+    _dev_check(momentum, _F32, "momentum")
+    _dev_check(param, _BF16, "param")
+    for name, t in [("momentum", momentum), ("param", param)] + [(f"grads[{r}]", g) for r, g in enumerate(grads)]:
+        if name.startswith("grads"):
+            _dev_check(t, _BF16, name)
+        if t.shape != master.shape:
+            raise ValueError(f"{name} is {tuple(t.shape)}, master {tuple(master.shape)}")
+    h = (hp if isinstance(hp, MuonHP) else MuonHP(**hp))._c()
+    ws, ws_bytes = _ns_workspace(workspace, rows, cols, batch, master.device, stream)
+    tab = (_vp * max(len(grads), 1))(*[g.data_ptr() for g in grads])
+    _q8_call(_lib.zs_reduce_muon, "zs_reduce_muon", (master, momentum, param, ws, *grads),
+             (tab, len(grads), batch, rows, cols, master.data_ptr(), momentum.data_ptr(), param.data_ptr(), ctypes.byref(h),
+              ws.data_ptr(), ws_bytes), stream)
 
 
 # ------------------------------------------------------------ optimizer offload
