@@ -508,34 +508,48 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ns_tile(const NsGemm a, uint32
   __syncthreads();                                  // and its space is free
 
   if (a.splits > 1) {
+    // The sums go past the XCD's own cache and are read the same way, by loads and stores of the whole device's scope: no
+    // cache is written back or emptied for them (fences of that scope, which do both, took 35 us a kernel).
     const int64_t tile = (int64_t)blockIdx.y * tiles + id;
-    float* mine = a.sums + (tile * a.splits + split) * (BM * BN);
+    uint64_t* const all_sums = (uint64_t*)(a.sums + tile * a.splits * (BM * BN));
+    uint64_t* mine = all_sums + (int64_t)split * (BM * BN / 2);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
-        *(GLB f32x4*)(GLB float*)(mine + (((wave * FM + i) * FN + j) * 64 + lane) * 4) = acc[i][j];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          __hip_atomic_store((GLB uint64_t*)mine + ((wave * FM + i) * FN + j) * 128 + q * 64 + lane,
+                             (uint64_t)__float_as_uint(acc[i][j][2 * q]) | (uint64_t)__float_as_uint(acc[i][j][2 * q + 1]) << 32,
+                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's sums are there for every other
     __syncthreads();
     if (tid == 0) {
       uint32_t* counter = a.counters + (int64_t)blockIdx.y * a.n_counters + id;
-      arrived = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+      arrived = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       // the last leaves the counter as it was found
       if (arrived == (uint32_t)a.splits - 1) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
     if (arrived != (uint32_t)a.splits - 1) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-    const float* from_first = a.sums + tile * a.splits * (BM * BN);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const float* p = from_first + (((wave * FM + i) * FN + j) * 64 + lane) * 4;
-        f32x4 v = *(const GLB f32x4*)(const GLB float*)p;
-        for (int s = 1; s < a.splits; ++s) v = v + *(const GLB f32x4*)(const GLB float*)(p + (int64_t)s * (BM * BN));
-        acc[i][j] = v;
-      }
+      for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
+    for (int s = 0; s < a.splits; ++s) {
+      const GLB uint64_t* from_split = (const GLB uint64_t*)all_sums + (int64_t)s * (BM * BN / 2);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint64_t w = __hip_atomic_load(from_split + ((wave * FM + i) * FN + j) * 128 + q * 64 + lane, __ATOMIC_RELAXED,
+                                                 __HIP_MEMORY_SCOPE_AGENT);
+            acc[i][j][2 * q] = acc[i][j][2 * q] + __uint_as_float((uint32_t)w);
+            acc[i][j][2 * q + 1] = acc[i][j][2 * q + 1] + __uint_as_float((uint32_t)(w >> 32));
+          }
+    }
   }
 
   // Results, 8 consecutive columns a lane.  Symmetric ones go to their mirrored place too, and the last step of a taller
@@ -626,24 +640,48 @@ int64_t tiles_of(int64_t m, int64_t n, int64_t side, bool triangle) {
   const int64_t tm = (m + side - 1) / side, tn = (n + side - 1) / side;
   return triangle ? tm * (tm + 1) / 2 : tm * tn;
 }
+// The tile and the split of a product, by the time its kernel takes (us, measured on 256 compute units): a start and an
+// end, and so much a stage of 32 for a few workgroups, for 256, and for 512 where two fit a unit; more go in rounds, which
+// overlap by half.  Split sums cost their exchange.  For example (rows x columns, product): 1024 x 1024, S: 10.8 in 64 x 64
+// tiles, 27 in 128 x 128, 64 in 256 x 256; 2048 x 2048, S 46 / 48 / 108, B X 62 / 55 / 108; 4096 x 4096, S 332 / 213 / 205, in 192
+// x 192 172, B X 419 / 305 / 275, in 192 x 192 328.  64 x 4096, S in 64 x 64 tiles: 26.6, in 2 splits 16.9, 8 10.1, 16 11.5.
+struct TileTime {
+  double start, few, full, twice;  // twice = 0: one a unit
+  double exchange, exchange_each;
+};
+constexpr TileTime kTileTime[4] = {{4.0, 0.175, 0.29, 0.45, 2.8, 0.35},
+                                   {5.5, 0.47, 0.78, 1.17, 4.0, 0.9},
+                                   {7.0, 0.83, 1.33, 0.0, 8.0, 2.0},
+                                   {10.0, 1.37, 2.1, 0.0, 12.0, 3.5}};
+double product_us(int t, int64_t groups, int64_t stages, int64_t splits) {
+  const TileTime& c = kTileTime[t];
+  const int64_t all = groups * splits, at_once = c.twice > 0 ? 512 : 256;
+  double stage;
+  if (all <= 256) {
+    stage = c.few + (c.full - c.few) * (double)all / 256;
+  } else if (all <= at_once) {
+    stage = c.full + (c.twice - c.full) * (double)(all - 256) / 256;
+  } else {
+    const double rounds = 0.5 * ((double)all / (double)at_once + (double)((all + at_once - 1) / at_once));
+    stage = (c.twice > 0 ? c.twice : c.full) * rounds;
+  }
+  return c.start + stage * (double)((stages + splits - 1) / splits) +
+         (splits > 1 ? c.exchange + c.exchange_each * (double)splits : 0.0);
+}
 Choice choose(int64_t m, int64_t n, int64_t k, int64_t batch, bool triangle) {
-  // us a stage of one round of workgroups, and how many a round has
-  constexpr double kStageUs[4] = {0.35, 0.70, 1.05, 1.60};
-  constexpr int kAtOnce[4] = {512, 512, 256, 256};
   const int64_t stages = k / 32;
   Choice best{NsTile::k64, 1, 0};
-  double least = 1e30;
+  double least = 1e300;
   for (int t = 0; t < 4; ++t) {
-    const int64_t tiles = tiles_of(m, n, kTileSide[t], triangle), groups = tiles * batch;
-    int64_t splits = kAtOnce[t] / groups;
-    const int64_t most = stages / 8;
-    splits = splits < most ? splits : most;
-    splits = splits > 32 ? 32 : splits < 1 ? 1 : splits;
-    const double rounds = (double)((groups * splits + kAtOnce[t] - 1) / kAtOnce[t]);
-    const double us = rounds * ((double)((stages + splits - 1) / splits) * kStageUs[t] + 2.0) + (splits > 1 ? 3.0 + 0.1 * (double)splits : 0.0);
-    if (us < least) {
-      least = us;
-      best = Choice{(NsTile)t, (int32_t)splits, tiles};
+    const int64_t tiles = tiles_of(m, n, kTileSide[t], triangle);
+    for (int64_t splits = 1; splits <= 16; splits *= 2) {
+      // split sums: of at most 512 workgroups, 4 stages each at least
+      if (splits > 1 && (tiles * batch * splits > 512 || stages < 4 * splits)) break;
+      const double us = product_us(t, tiles * batch, stages, splits);
+      if (us < least) {
+        least = us;
+        best = Choice{(NsTile)t, (int32_t)splits, tiles};
+      }
     }
   }
   return best;
