@@ -5,6 +5,8 @@
 //   kWeight   dWg = dgate^T x, dWu = dup^T x      (+ earlier micro-batches' sums), two products in one launch
 //
 // Operands are bf16 or fp16, sums fp32, each output rounded once.
+#include <cmath>
+
 #include "zs_act.h"
 #include "zs_glu.h"
 #include "zs_tile_dev.h"
@@ -121,22 +123,23 @@ __device__ __forceinline__ i32x4 inside(int left) {
 // ---------------------------------------------------------------------------
 // Rows at any address: 64 x 64 sums per workgroup of four waves (32 x 32 each),
 // operands staged through registers 16 bytes at a time, 64 of the summed axis a
-// step.  Forward: 32 columns of gate beside the same 32 of up.
+// stage, four stages ahead of the matrix instructions; two buffers in LDS and
+// one barrier a stage.  Forward: 32 columns of gate beside the same 32 of up.
 // ---------------------------------------------------------------------------
 constexpr int kAnyTile = 64;
 constexpr int kStage = 64;  // of the summed axis a stage: 128 bytes of a row
 
 template <GluOp OP, int FMT>
 __global__ __launch_bounds__(256) void glu_any(const GluGemm a, int64_t tiles_n, int64_t tiles) {
-  constexpr bool kARow = OP != GluOp::kWeight, kBRow = OP == GluOp::kForward;
-  constexpr int kOutN = OP == GluOp::kForward ? 32 : 64;
-  __shared__ __attribute__((aligned(16))) char lds_a[8192];
-  __shared__ __attribute__((aligned(16))) char lds_b[8192];
+  constexpr bool kForward = OP == GluOp::kForward, kInput = OP == GluOp::kInput, kWeight = OP == GluOp::kWeight;
+  constexpr bool kARow = !kWeight, kBRow = kForward;
+  constexpr int kOutN = kForward ? 32 : 64, kAhead = 4;
+  __shared__ __attribute__((aligned(16))) char lds[2][2][8192];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
   const int g = lane >> 4, i16 = lane & 15;
-  constexpr int kParts = OP == GluOp::kForward ? 1 : 2;  // kInput: summed; kWeight: side by side
-  const int64_t all = OP == GluOp::kWeight ? 2 * tiles : tiles;
+  const int64_t nk = (a.K + kStage - 1) / kStage, stages = kInput ? 2 * nk : nk;
+  const int64_t all = kWeight ? 2 * tiles : tiles;
   for (int64_t at = blockIdx.x; at < all; at += gridDim.x) {
     const int out = at >= tiles ? 1 : 0;
     const int64_t tile = at - out * tiles;
@@ -146,51 +149,59 @@ __global__ __launch_bounds__(256) void glu_any(const GluGemm a, int64_t tiles_n,
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
-    for (int part = 0; part < (OP == GluOp::kInput ? kParts : 1); ++part) {
-      const int pa = OP == GluOp::kInput ? part : out;
-      const char* pa_base = (const char*)a.a[OP == GluOp::kForward ? 0 : pa];
-      const char* pb_base = (const char*)a.b[OP == GluOp::kInput ? part : 0];
-      for (int64_t k0 = 0; k0 < a.K; k0 += kStage) {
-        u32x4 ra[2], rb[2];
+    u32x4 ra[kAhead][2], rb[kAhead][2];
+    auto fetch = [&](int64_t stage, int u) {
+      const bool second = kInput && stage >= nk, live = stage < stages;
+      const int64_t k0 = (second ? stage - nk : stage) * kStage;
+      const char* base_a = (const char*)a.a[kForward ? 0 : kWeight ? out : second];
+      const char* base_b = (const char*)a.b[kInput ? second : 0];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int p = tid + 256 * c, row = p / 8, col = p % 8 * 16;  // 8 pieces a row of 64 values
-          if constexpr (kARow) {
-            const int64_t m = m0 + row;
-            ra[c] = ld_piece<2>(pa_base + m * a.lda * 2, k0 * 2 + col, a.K * 2, m < a.M);
-          } else {
-            const int64_t k = k0 + row;
-            ra[c] = ld_piece<2>(pa_base + k * a.lda * 2, m0 * 2 + col, a.M * 2, k < a.K);
-          }
-          if constexpr (kBRow) {  // rows 0 .. 31 of gate, then of up
-            const int64_t n = n0 + row % 32;
-            rb[c] = ld_piece<2>((const char*)a.b[row / 32] + n * a.ldb * 2, k0 * 2 + col, a.K * 2, n < a.N);
-          } else {
-            const int64_t k = k0 + row;
-            rb[c] = ld_piece<2>(pb_base + k * a.ldb * 2, n0 * 2 + col, a.N * 2, k < a.K);
-          }
+      for (int c = 0; c < 2; ++c) {
+        const int p = tid + 256 * c, row = p / 8, col = p % 8 * 16;  // 8 pieces a row of 64 values
+        const int64_t k = k0 + row;
+        if constexpr (kARow) {
+          const int64_t m = m0 + row;
+          ra[u][c] = ld_piece<2>(base_a + m * a.lda * 2, k0 * 2 + col, a.K * 2, live && m < a.M);
+        } else {
+          ra[u][c] = ld_piece<2>(base_a + k * a.lda * 2, m0 * 2 + col, a.M * 2, live && k < a.K);
         }
-        __syncthreads();  // the step before has been read
-        auto place = [](int row, int piece, bool by_row) {
-          return row * 128 + (piece ^ (by_row ? row & 7 : (row & 3) << 1)) * 16;
-        };
+        if constexpr (kBRow) {  // rows 0 .. 31 of gate, then of up
+          const int64_t n = n0 + row % 32;
+          rb[u][c] = ld_piece<2>((const char*)a.b[row / 32] + n * a.ldb * 2, k0 * 2 + col, a.K * 2, live && n < a.N);
+        } else {
+          rb[u][c] = ld_piece<2>(base_b + k * a.ldb * 2, n0 * 2 + col, a.N * 2, live && k < a.K);
+        }
+      }
+    };
+    auto place = [](int row, int piece, bool by_row) { return row * 128 + (piece ^ (by_row ? row & 7 : (row & 3) << 1)) * 16; };
+    auto by_row = [&](const char* base, int r, int half) {
+      return *(const i32x4*)(base + r * 128 + ((4 * half + g) ^ (r & 7)) * 16);
+    };
+    auto turned = [&](const char* base, int col, int half) {  // 8 rows of the summed axis x 16 columns
+      const int row = 32 * half + 8 * g + (i16 >> 2);
+      const char* q = base + row * 128 + ((col / 8 + (i16 >> 1 & 1)) ^ (row & 3) << 1) * 16 + (i16 & 1) * 8;
+      const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)q);
+      const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(q + 4 * 128));
+      return __builtin_bit_cast(i32x4, (i16x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+    };
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) fetch(u, u);
+    for (int64_t s0 = 0; s0 < stages; s0 += kAhead) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {  // (stages past the last are zeros)
+        char* const lds_a = lds[u & 1][0];
+        char* const lds_b = lds[u & 1][1];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int p = tid + 256 * c;
-          *(u32x4*)(lds_a + place(p / 8, p % 8, kARow)) = ra[c];
-          *(u32x4*)(lds_b + place(p / 8, p % 8, kBRow)) = rb[c];
+          *(u32x4*)(lds_a + place(p / 8, p % 8, kARow)) = ra[u][c];
+          *(u32x4*)(lds_b + place(p / 8, p % 8, kBRow)) = rb[u][c];
         }
-        __syncthreads();
-        auto by_row = [&](const char* base, int r, int half) {
-          return *(const i32x4*)(base + r * 128 + ((4 * half + g) ^ (r & 7)) * 16);
-        };
-        auto turned = [&](const char* base, int col, int half) {  // 8 rows of the summed axis x 16 columns
-          const int row = 32 * half + 8 * g + (i16 >> 2);
-          const char* q = base + row * 128 + ((col / 8 + (i16 >> 1 & 1)) ^ (row & 3) << 1) * 16 + (i16 & 1) * 8;
-          const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)q);
-          const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(q + 4 * 128));
-          return __builtin_bit_cast(i32x4, (i16x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
-        };
+        fetch(s0 + u + kAhead, u);
+        // what is written here was read two stages ago, before the barrier in between
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           i32x4 fa[2], fb[2];
@@ -215,7 +226,7 @@ __global__ __launch_bounds__(256) void glu_any(const GluGemm a, int64_t tiles_n,
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int64_t m = m0 + wm + i * 16 + i16;
-      if constexpr (OP == GluOp::kForward) {
+      if constexpr (kForward) {
         float gate[4], up[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) gate[r] = acc[i][0][r], up[r] = acc[i][1][r];
@@ -228,7 +239,7 @@ __global__ __launch_bounds__(256) void glu_any(const GluGemm a, int64_t tiles_n,
           float v[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) v[r] = acc[i][j][r];
-          if constexpr (OP == GluOp::kInput)
+          if constexpr (kInput)
             store_run_as<FMT, 4, false>(a.out[0], nullptr, m * a.ldo[0] + n, a.N - n, v);
           else
             store_grad<FMT, 4>(a, out, m * a.ldo[out] + n, a.N - n, v);
@@ -265,7 +276,7 @@ hipError_t any_launch(const GluGemm& a, hipStream_t stream) {
 // the same 32 of up, so that a lane ends with 8 columns of both.
 // ---------------------------------------------------------------------------
 template <GluOp OP, int FMT, int BM, int BN, int WM, int WN, int NS, bool PAST>
-__global__ __launch_bounds__(WM* WN * 64, 2) void glu_tile(const GluGemm a, uint32_t tiles_m, uint32_t tiles_n) {
+__global__ __launch_bounds__(WM* WN * 64, NS*(BM + BN) * 128 > 81920 && WM * WN == 4 ? 1 : 2) void glu_tile(const GluGemm a, uint32_t tiles_m, uint32_t tiles_n) {
   constexpr bool kForward = OP == GluOp::kForward, kInput = OP == GluOp::kInput, kWeight = OP == GluOp::kWeight;
   constexpr bool kARow = !kWeight, kBRow = kForward;
   constexpr int kWaves = WM * WN, kOutN = kForward ? BN / 2 : BN;
@@ -275,7 +286,11 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void glu_tile(const GluGemm a, uint
   constexpr int kABytes = kARow ? BM * 128 : 8 * kAGroup, kBBytes = kBRow ? BN * 128 : 8 * kBGroup;
   constexpr int kBuf = kABytes + kBBytes;
   constexpr int kALoads = BM / 8 / kWaves, kBLoads = BN / 8 / kWaves;
-  static_assert(FN % 2 == 0 && kALoads > 0 && kBLoads > 0 && (NS & (NS - 1)) == 0 && (!kForward || (TN == 64 && kBLoads <= 4)),
+  // Forward: a wave's 64 columns are 32 of gate and 32 of up; a narrow tile's 32 are 16 and 16
+  constexpr bool kNarrow = kForward && TN == 32;
+  constexpr int kUpAt = TN / 16;  // b's loads of 8 rows: so many, half of gate and half of up
+  static_assert(FN % 2 == 0 && kALoads > 0 && kBLoads > 0 && (NS & (NS - 1)) == 0 && (!kForward || TN == 64 || TN == 32) &&
+                    (!kForward || kUpAt % kBLoads == 0),
                 "tile shape");
   __shared__ __attribute__((aligned(1024))) char lds[NS * kBuf];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -310,14 +325,15 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void glu_tile(const GluGemm a, uint
   uint32_t vb_row[2];
 #pragma unroll
   for (int p = 0; p < 2; ++p)
-    vb_row[p] = (uint32_t)(lane >> 3) * (uint32_t)pitch_b + (uint32_t)(((lane & 7) ^ ((lane >> 3 & 3) | p << 2)) * 16);
+    vb_row[p] = (uint32_t)(lane >> 3) * (uint32_t)pitch_b + (uint32_t)(((lane & 7) ^ (kNarrow ? lane >> 3 : (lane >> 3 & 3) | p << 2)) * 16);
   // A stage past the last lies past the end of every buffer: zeros, and no traffic.
   auto from = [&](int stage) { return stage < stages ? (uint32_t)(k_of(stage) * 2) : 0x7FFFFFF0u; };
   // Across it: piece c of row r at place c ^ s(r).  A transposing read takes 32 bytes of 4 consecutive rows, and of 4
   // that lie 8 rows on, per 32 lanes: s puts those 4 at different places.
   auto s_of = [](int row) { return (row & 3) << 1; };
   constexpr int kAPer = BM / 8, kBPer = BN / 8;            // pieces in a row
-  constexpr int kARows = 64 / kAPer, kBRows = 64 / kBPer;  // rows a load
+  constexpr int kARows = 64 / kAPer, kBRows = 64 / kBPer;  // rows a load (across the axis)
+  static_assert((kARow || 64 % kAPer == 0) && (kBRow || 64 % kBPer == 0), "whole rows a load");
   constexpr int kAApart = kARows >= 4 ? 1 : 4 / kARows, kBApart = kBRows >= 4 ? 1 : 4 / kBRows;  // loads to the same s
   uint32_t va_col[kAApart], vb_col[kBApart];
 #pragma unroll
@@ -332,7 +348,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void glu_tile(const GluGemm a, uint
   }
 
   // Forward: this wave's loads of b are all of gate or all of up.
-  const int up = kForward ? wave * kBLoads / 4 % 2 : 0;
+  const int up = kForward ? wave * kBLoads / kUpAt % 2 : 0;
   const Rsrc rb_row = make_rsrc((const char*)a.b[up] + n0 * a.ldb * 2, cols_b, K * 2, pitch_b);
   auto load_a = [&](int stage, int j) {
     const int t = wave * kALoads + j;
@@ -350,7 +366,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void glu_tile(const GluGemm a, uint
     const int t = wave * kBLoads + j;
     const uint32_t to = lds0 + (stage & (NS - 1)) * kBuf + kABytes;
     if constexpr (kBRow) {
-      const int row = t / 8 * 32 + t % 4 * 8;  // of gate or up
+      const int row = t / (2 * kUpAt) * (TN / 2) + t % kUpAt * 8;  // of gate or up
       load_to_lds(rb_row, vb_row[t & 1] + (uint32_t)row * (uint32_t)pitch_b + from(stage), to + t * 1024);
     } else {
       const Rsrc r = make_rsrc(b_of(stage) + (k_of(stage) * a.ldb + n0) * 2, rows_at(stage), cols_b * 2, pitch_b);
@@ -368,7 +384,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void glu_tile(const GluGemm a, uint
 
   const int s7 = i16 & 7;
   const int at_a_row = (wm + i16) * 128;
-  const int at_b_row = kABytes + (wn + (i16 >> 2) * 8 + (i16 & 3)) * 128;
+  const int at_b_row = kABytes + (wn + (kNarrow ? i16 : (i16 >> 2) * 8 + (i16 & 3))) * 128;
   // A lane's place in the rows of a transposing read of 16 columns from 16 c on.
   auto place_of = [&](int group, int pitch, int c) {
     return (uint32_t)(g * group + (i16 >> 2) * pitch + ((2 * (c & 3) + (i16 >> 1 & 1)) ^ (i16 >> 2) << 1) * 16 + (i16 & 1) * 8 +
@@ -395,8 +411,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void glu_tile(const GluGemm a, uint
   };
   auto read_b = [&](int buf, int half, int j) {
     if constexpr (kBRow)
-      fb[half][j] = *(const LDS i32x4*)((LDS char*)lds + buf * kBuf + at_b_row + (j / 2 * 32 + j % 2 * 4) * 128 +
-                                        ((4 * half + g) ^ s7) * 16);
+      fb[half][j] = *(const LDS i32x4*)((LDS char*)lds + buf * kBuf + at_b_row +
+                                        (kNarrow ? j * 16 : j / 2 * 32 + j % 2 * 4) * 128 + ((4 * half + g) ^ s7) * 16);
     else
       fb[half][j] = turned(place_b[j % kBPlaces] + (uint32_t)(buf * kBuf + half * 4 * kBGroup + j / 4 * 128), 4 * BN * 2);
   };
@@ -470,7 +486,12 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void glu_tile(const GluGemm a, uint
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int64_t m = m0 + wm + i * 16 + i16;
-    if constexpr (kForward) {
+    if constexpr (kNarrow) {
+      float v[2][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[0][r] = acc[i][0][r], v[1][r] = acc[i][1][r];
+      store_gated<FMT, 4, false>(a, m, n0 + wn / 2 + g * 4, v[0], v[1]);
+    } else if constexpr (kForward) {
       float v[2][8];
 #pragma unroll
       for (int r = 0; r < 8; ++r) v[0][r] = acc[i][r / 4][r % 4], v[1][r] = acc[i][2 + r / 4][r % 4];
@@ -514,6 +535,168 @@ hipError_t tile_launch(const GluGemm& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Few tokens, forward: 16 rows, and 16 columns of gate and the same 16 of up,
+// per workgroup, whose W waves take every W-th 32 of the summed axis.  Fragments
+// go from memory straight into registers, eight steps ahead, and no wave waits
+// for another until their sums meet in LDS, where they are added in the waves'
+// order: a stage of the tiled kernels takes at least 0.2 us, whatever its size,
+// for its barrier and two rounds of LDS reads.  With 32 or 64 rows a workgroup it
+// lost to the tiles (61 x 4096 x 4096: 32 and 24 us, 18 in 64 x 32).  One token, N =
+// 11008, K = 4096: 36-40 us by every kernel here, the weights' 180 MB at 4.5-5 TB/s.
+// ---------------------------------------------------------------------------
+template <int FMT, int W>
+__global__ __launch_bounds__(W * 64, 2) void glu_few(const GluGemm a, uint32_t tiles_n) {
+  constexpr int kAhead = 8, kPitch = 20;
+  __shared__ __attribute__((aligned(16))) float lds[W][2][16 * kPitch];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, i16 = lane & 15;
+  const int64_t n0 = (int64_t)(blockIdx.x % tiles_n) * 16, m0 = (int64_t)(blockIdx.x / tiles_n) * 16;
+  const int32_t K = (int32_t)a.K, steps = (K + 31) / 32;
+  const int32_t pitch_a = (int32_t)a.lda * 2, pitch_b = (int32_t)a.ldb * 2, cols = left_of(a.N, n0, 16);
+  const Rsrc ra = make_rsrc((const char*)a.a[0] + m0 * a.lda * 2, left_of(a.M, m0, 16), K * 2, pitch_a);
+  const Rsrc rg = make_rsrc((const char*)a.b[0] + n0 * a.ldb * 2, cols, K * 2, pitch_b);
+  const Rsrc ru = make_rsrc((const char*)a.b[1] + n0 * a.ldb * 2, cols, K * 2, pitch_b);
+  const uint32_t va = (uint32_t)(i16 * pitch_a + g * 16), vb = (uint32_t)(i16 * pitch_b + g * 16);
+  f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  i32x4 fa[kAhead], fb[kAhead][2];
+  // (a step past the last is not fetched: its offset could lie in the next row)
+  auto fetch = [&](int step, int u) {
+    const uint32_t off = step < steps ? (uint32_t)step * 64u : 0x7FFFFFF0u;
+    fb[u][0] = __builtin_bit_cast(i32x4, ld_buffer16(rg, vb + off));
+    fb[u][1] = __builtin_bit_cast(i32x4, ld_buffer16(ru, vb + off));
+    fa[u] = __builtin_bit_cast(i32x4, ld_buffer16(ra, va + off));
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) fetch(wave + u * W, u);
+  for (int step = wave; step < steps; step += kAhead * W) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int at = step + u * W;
+      if (at * 32 + 32 > K) {  // the end of the axis, or past it: what the rows go on with may not be finite
+        const i32x4 mask = inside(K - at * 32 - 8 * g);
+        fa[u] &= mask;
+        fb[u][0] &= mask;
+        fb[u][1] &= mask;
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p) acc[p] = mfma16<FMT>(fb[u][p], fa[u], acc[p]);
+      fetch(at + kAhead * W, u);
+    }
+  }
+  // sums: row i16, columns 4 g .. 4 g + 3
+#pragma unroll
+  for (int p = 0; p < 2; ++p) *(f32x4*)(&lds[wave][p][i16 * kPitch + 4 * g]) = acc[p];
+  __syncthreads();
+  if (tid >= 64) return;
+  const int row = tid / 4, four = tid % 4 * 4;
+  float v[2][4];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    f32x4 sum = *(const f32x4*)(&lds[0][p][row * kPitch + four]);
+#pragma unroll
+    for (int w = 1; w < W; ++w) sum = sum + *(const f32x4*)(&lds[w][p][row * kPitch + four]);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[p][r] = sum[r];
+  }
+  store_gated<FMT, 4, false>(a, m0 + row, n0 + four, v[0], v[1]);
+}
+
+template <int FMT, int W>
+hipError_t few_launch(const GluGemm& a, hipStream_t stream) {
+  const uint32_t tn = (uint32_t)((a.N + 15) / 16), tm = (uint32_t)((a.M + 15) / 16);
+  glu_few<FMT, W><<<dim3(tm * tn), W * 64, 0, stream>>>(a, tn);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens, input gradient: 16 x 64 sums per workgroup, whose eight waves take
+// every eighth 32 of the summed axis (both pairs of operands one behind the
+// other), loaded into a part of LDS of the wave's own, three steps ahead, where
+// the weights' rows are turned.  The waves' sums are added in their order.
+// ---------------------------------------------------------------------------
+template <int FMT>
+__global__ __launch_bounds__(512, 2) void glu_input_split(const GluGemm a, uint32_t tiles_m, uint32_t tiles_n) {
+  constexpr int kWaves = 8, kAhead = 3, kOps = 5;
+  constexpr int kAtB = 1024, kBuf = kAtB + 32 * 128;  // 16 rows of 32 values; 32 rows of 64 columns
+  constexpr int kPitch = 68;                          // floats from row to row of the sums
+  __shared__ __attribute__((aligned(1024))) char lds[kWaves * kAhead * kBuf];
+  static_assert(sizeof(lds) >= kWaves * 16 * kPitch * 4, "sums");
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, i16 = lane & 15;
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * 16, n0 = (int64_t)tn * 64;
+  const int32_t K = (int32_t)a.K, half = (K + 31) / 32, steps = 2 * half;
+  const int32_t pitch_a = (int32_t)a.lda * 2, pitch_b = (int32_t)a.ldb * 2;
+  const int32_t rows = left_of(a.M, m0, 16), cols = left_of(a.N, n0, 64);
+  const uint32_t mine = (uint32_t)(uintptr_t)(LDS char*)lds + wave * kAhead * kBuf;
+  // a: 4 pieces a row, piece c of row r at place c ^ (r / 2 % 4); b: 8 pieces a row, at place c ^ s(r)
+  auto s_of = [](int r) { return (r & 3) << 1; };
+  const uint32_t va = (uint32_t)((lane >> 2) * pitch_a + ((lane & 3) ^ (lane >> 3 & 3)) * 16);
+  auto fetch = [&](int step, int buf) {
+    const bool second = step >= half;
+    const int32_t k0 = (second ? step - half : step) * 32;
+    const int32_t left = step < steps ? (K - k0 < 32 ? K - k0 : 32) : 0;
+    const Rsrc ra = make_rsrc((const char*)(second ? a.a[1] : a.a[0]) + m0 * a.lda * 2, rows, K * 2, pitch_a);
+    const Rsrc rb = make_rsrc((const char*)(second ? a.b[1] : a.b[0]) + ((int64_t)k0 * a.ldb + n0) * 2, left, cols * 2, pitch_b);
+    load_to_lds(ra, va + (step < steps ? (uint32_t)k0 * 2u : 0x7FFFFFF0u), mine + buf * kBuf);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = j * 8 + (lane >> 3);
+      load_to_lds(rb, (uint32_t)(row * pitch_b + ((lane & 7) ^ s_of(row)) * 16), mine + buf * kBuf + kAtB + j * 1024);
+    }
+  };
+  f32x4 acc[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc[j] = (f32x4){0, 0, 0, 0};
+#pragma unroll
+  for (int p = 0; p < kAhead; ++p) fetch(wave + p * kWaves, p);
+  int buf = 0;
+  for (int step = wave; step < steps; step += kWaves) {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kAhead - 1) * kOps) : "memory");
+    LDS char* p = (LDS char*)lds + (wave * kAhead + buf) * kBuf;
+    i32x4 fa = *(LDS i32x4*)(p + i16 * 64 + (g ^ (i16 >> 1 & 3)) * 16);
+    i32x4 fb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = 8 * g + (i16 >> 2);
+      LDS char* q = p + kAtB + row * 128 + ((2 * j + (i16 >> 1 & 1)) ^ s_of(row)) * 16 + (i16 & 1) * 8;
+      const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)q);
+      const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(q + 4 * 128));
+      fb[j] = __builtin_bit_cast(i32x4, (i16x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // all of the buffer is read
+    fetch(step + kAhead * kWaves, buf);
+    const int left = K - (step >= half ? step - half : step) * 32;
+    if (left < 32) fa &= inside(left - 8 * g);  // rows of b past the end are zeros
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = mfma16<FMT>(fb[j], fa, acc[j]);
+    buf = buf == kAhead - 1 ? 0 : buf + 1;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way to LDS
+  __syncthreads();
+  float* sums = (float*)lds;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) *(f32x4*)(sums + (wave * 16 + i16) * kPitch + j * 16 + g * 4) = acc[j];
+  __syncthreads();
+  if (tid >= 256) return;
+  const int row = tid / 16, col = tid % 16 * 4;
+  f32x4 v = *(const f32x4*)(sums + row * kPitch + col);
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) v = v + *(const f32x4*)(sums + (w * 16 + row) * kPitch + col);
+  const int64_t m = m0 + row, n = n0 + col;
+  const float out[4] = {v[0], v[1], v[2], v[3]};
+  if (m < a.M && n < a.N) store_run_as<FMT, 4, false>(a.out[0], nullptr, m * a.ldo[0] + n, a.N - n, out);
+}
+
+template <int FMT>
+hipError_t input_split_launch(const GluGemm& a, hipStream_t stream) {
+  const uint32_t tm = (uint32_t)((a.M + 15) / 16), tn = (uint32_t)((a.N + 63) / 64);
+  glu_input_split<FMT><<<dim3(tm * tn), 512, 0, stream>>>(a, tm, tn);
+  return hipGetLastError();
+}
+
 // Rows that the tiled kernels take: on 16-byte boundaries (a single row at any
 // distance from the next), offsets within a tile below 2^31, a grid that a
 // launch can hold.
@@ -522,6 +705,49 @@ bool rows16(const void* p, int64_t rows, int64_t ld) {
 }
 int64_t tiles_of(const GluGemm& a, int64_t bm, int64_t bn) { return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn); }
 constexpr int64_t kMostTiles = 1 << 22;
+
+// The kernel of a product with 16-byte rows, by the time it takes: a start, and so much a stage of 64 of the summed axis,
+// between `few` for a few workgroups and `full` for as many as run at once; more go in rounds (half overlapped) with a
+// start of their own.  us, fitted to 54 shapes from 1 to 9683 tokens on 256 compute units, inputs from memory: off by 6 to
+// 20%, and what it picks is 1.0 to 1.8% behind the best kernel's time in the mean.  For example, forward: 1 x 1024 x 1024 4.9 by
+// kFew, 6.4 by k64x32, 7.8 by k64; 61 x 4096 x 4096 55 / 18.1 / 20.7, 27.2 by k128; 333 x 11008 x 4096 136 by k64, 96 by k128, 88 by k192,
+// 100 by k256; input gradient: 61 x 4096 x 4096 23.9 by kSplit, 37 by k32, 67 by k128; 1025 x 1376 x 4096 118 by kSplit, 56 by k128, 43 by
+// k128Near, 60 by k256; weight gradients: 61 x 4096 x 4096 25.7 by k64, 22.9 by k128Near, 20.4 by k256.
+enum class GluTile { kFew, kFew8, kSplit, k64x32, k32, k64, k64x128, k128, k128Near, k192, k256 };
+struct TileCost {
+  GluTile tile;
+  int bm, bn, at_once;  // sums of a workgroup; workgroups at once
+  double start, few, full, round;
+};
+constexpr TileCost kForwardCosts[] = {{GluTile::kFew, 16, 32, 2048, 3.68, 0.089, 1.459, 0.0},
+                                      {GluTile::kFew8, 16, 32, 1024, 5.72, 0.088, 0.635, 5.45},
+                                      {GluTile::k64x32, 64, 32, 256, 3.74, 0.200, 0.237, 1.24},
+                                      {GluTile::k64, 64, 64, 512, 3.80, 0.243, 0.455, 0.40},
+                                      {GluTile::k128, 128, 128, 256, 4.07, 0.337, 0.521, 2.13},
+                                      {GluTile::k192, 192, 128, 512, 2.17, 0.700, 1.256, 1.61},
+                                      {GluTile::k256, 256, 256, 256, 3.42, 1.128, 1.525, 3.95}};
+constexpr TileCost kInputCosts[] = {{GluTile::kSplit, 16, 64, 256, 3.02, 0.124, 0.165, 1.30},
+                                    {GluTile::k32, 32, 64, 512, 3.40, 0.248, 0.334, 0.72},
+                                    {GluTile::k64x128, 64, 128, 256, 4.54, 0.356, 0.435, 1.48},
+                                    {GluTile::k128, 128, 128, 256, 4.18, 0.471, 0.612, 2.13},
+                                    {GluTile::k128Near, 128, 128, 512, 2.15, 0.722, 1.063, 1.60},
+                                    {GluTile::k256, 256, 256, 256, 3.96, 1.179, 1.622, 0.0}};
+constexpr TileCost kWeightCosts[] = {{GluTile::k64, 64, 64, 1024, 3.99, 0.294, 0.745, 2.01},
+                                     {GluTile::k128, 128, 128, 256, 5.14, 0.406, 0.527, 2.55},
+                                     {GluTile::k128Near, 128, 128, 512, 6.59, 0.460, 0.899, 3.05},
+                                     {GluTile::k256, 256, 256, 256, 8.99, 1.156, 1.454, 5.34}};
+template <size_t N>
+GluTile cheapest(const TileCost (&costs)[N], const GluGemm& a, int64_t wide, int64_t parts, int64_t stages) {
+  double least = 1e300;
+  GluTile best = costs[N - 1].tile;
+  for (const TileCost& c : costs) {
+    const double x = (double)(parts * ((a.M + c.bm - 1) / c.bm) * ((wide + c.bn - 1) / c.bn)) / c.at_once;
+    const double stage = c.few + (c.full - c.few) * (x < 1 ? x : 1);
+    const double us = x <= 1 ? c.start + stage * (double)stages : c.start + 0.5 * (x + std::ceil(x)) * (c.round + stage * (double)stages);
+    if (us < least) least = us, best = c.tile;
+  }
+  return best;
+}
 
 template <GluOp OP, int FMT>
 hipError_t gemm_launch(const GluGemm& given, hipStream_t stream) {
@@ -537,13 +763,34 @@ hipError_t gemm_launch(const GluGemm& given, hipStream_t stream) {
   const int64_t wide_a = weight ? 256 : a.K, wide_b = forward ? a.K : 256;
   if (rows_a <= 1) a.lda = (wide_a + 255) / 256 * 256;
   if (rows_b <= 1) a.ldb = (wide_b + 255) / 256 * 256;
-  const int64_t parts = weight ? 2 : 1, half = forward ? 2 : 1;
-  const int64_t t256 = parts * tiles_of(a, 256, 256 / half), t128 = parts * tiles_of(a, 128, 128 / half),
-                t64 = parts * tiles_of(a, 64, 64 / half);
-  if (t64 <= 256) return tile_launch<OP, FMT, 64, 64, 4, 1, 4>(a, stream);
-  if (t128 <= 256) return tile_launch<OP, FMT, 128, 128, 4, 2, 4>(a, stream);
-  if (t256 <= 200) return tile_launch<OP, FMT, 128, 128, 2, 2, 2>(a, stream);
-  return tile_launch<OP, FMT, 256, 256, 2, 4, 2>(a, stream);
+  const int64_t stages = (a.K + kStage - 1) / kStage;
+  if constexpr (OP == GluOp::kForward) {
+    switch (cheapest(kForwardCosts, a, 2 * a.N, 1, stages)) {
+      case GluTile::kFew: return few_launch<FMT, 4>(a, stream);
+      case GluTile::kFew8: return few_launch<FMT, 8>(a, stream);
+      case GluTile::k64x32: return tile_launch<OP, FMT, 64, 32, 4, 1, 8>(a, stream);
+      case GluTile::k64: return tile_launch<OP, FMT, 64, 64, 4, 1, 4>(a, stream);
+      case GluTile::k128: return tile_launch<OP, FMT, 128, 128, 4, 2, 4>(a, stream);
+      case GluTile::k192: return tile_launch<OP, FMT, 192, 128, 4, 2, 2>(a, stream);
+      default: return tile_launch<OP, FMT, 256, 256, 2, 4, 2>(a, stream);
+    }
+  } else if constexpr (OP == GluOp::kInput) {
+    switch (cheapest(kInputCosts, a, a.N, 1, 2 * stages)) {
+      case GluTile::kSplit: return input_split_launch<FMT>(a, stream);
+      case GluTile::k32: return tile_launch<OP, FMT, 32, 64, 2, 2, 4>(a, stream);
+      case GluTile::k64x128: return tile_launch<OP, FMT, 64, 128, 2, 2, 4>(a, stream);
+      case GluTile::k128: return tile_launch<OP, FMT, 128, 128, 4, 2, 4>(a, stream);
+      case GluTile::k128Near: return tile_launch<OP, FMT, 128, 128, 2, 2, 2>(a, stream);
+      default: return tile_launch<OP, FMT, 256, 256, 2, 4, 2>(a, stream);
+    }
+  } else {
+    switch (cheapest(kWeightCosts, a, a.N, 2, stages)) {
+      case GluTile::k64: return tile_launch<OP, FMT, 64, 64, 4, 1, 2>(a, stream);
+      case GluTile::k128: return tile_launch<OP, FMT, 128, 128, 4, 2, 4>(a, stream);
+      case GluTile::k128Near: return tile_launch<OP, FMT, 128, 128, 2, 2, 2>(a, stream);
+      default: return tile_launch<OP, FMT, 256, 256, 2, 4, 2>(a, stream);
+    }
+  }
 }
 
 template <GluOp OP>
