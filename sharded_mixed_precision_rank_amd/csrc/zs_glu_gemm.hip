@@ -150,24 +150,47 @@ __global__ __launch_bounds__(256) void glu_any(const GluGemm a, int64_t tiles_n,
 #pragma unroll
       for (int j = 0; j < 2; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
     u32x4 ra[kAhead][2], rb[kAhead][2];
+    // A thread's pieces: rows tid / 8 and 32 on, bytes tid % 8 * 16
+    const int row = tid / 8, col = tid % 8 * 16;
+    // Forward, inside the summed axis: no bounds to look at (490 x 752 x 7392, rows one element off: 50 us, was 126; the
+    // others lost by a second path).  Rows behind the last, whose sums are not stored, are the last one again.
+    const char* fast_a[2] = {};
+    const char* fast_b[2] = {};
+    if constexpr (kForward) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int64_t m = m0 + row + 32 * c, n = n0 + row;  // (rows 0 .. 31 of gate, then of up)
+        fast_a[c] = (const char*)a.a[0] + (m < a.M ? m : a.M - 1) * a.lda * 2 + col;
+        fast_b[c] = (const char*)a.b[c] + (n < a.N ? n : a.N - 1) * a.ldb * 2 + col;
+      }
+    }
     auto fetch = [&](int64_t stage, int u) {
       const bool second = kInput && stage >= nk, live = stage < stages;
       const int64_t k0 = (second ? stage - nk : stage) * kStage;
+      if constexpr (kForward) {
+        if (k0 + kStage <= a.K) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            ra[u][c] = ld_any<u32x4>((const uint16_t*)(fast_a[c] + k0 * 2));
+            rb[u][c] = ld_any<u32x4>((const uint16_t*)(fast_b[c] + k0 * 2));
+          }
+          return;
+        }
+      }
       const char* base_a = (const char*)a.a[kForward ? 0 : kWeight ? out : second];
       const char* base_b = (const char*)a.b[kInput ? second : 0];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int p = tid + 256 * c, row = p / 8, col = p % 8 * 16;  // 8 pieces a row of 64 values
-        const int64_t k = k0 + row;
+        const int64_t k = k0 + row + 32 * c;
         if constexpr (kARow) {
-          const int64_t m = m0 + row;
+          const int64_t m = m0 + row + 32 * c;
           ra[u][c] = ld_piece<2>(base_a + m * a.lda * 2, k0 * 2 + col, a.K * 2, live && m < a.M);
         } else {
           ra[u][c] = ld_piece<2>(base_a + k * a.lda * 2, m0 * 2 + col, a.M * 2, live && k < a.K);
         }
-        if constexpr (kBRow) {  // rows 0 .. 31 of gate, then of up
-          const int64_t n = n0 + row % 32;
-          rb[u][c] = ld_piece<2>((const char*)a.b[row / 32] + n * a.ldb * 2, k0 * 2 + col, a.K * 2, live && n < a.N);
+        if constexpr (kBRow) {
+          const int64_t n = n0 + row;
+          rb[u][c] = ld_piece<2>((const char*)a.b[c] + n * a.ldb * 2, k0 * 2 + col, a.K * 2, live && n < a.N);
         } else {
           rb[u][c] = ld_piece<2>(base_b + k * a.ldb * 2, n0 * 2 + col, a.N * 2, live && k < a.K);
         }
@@ -261,7 +284,7 @@ hipError_t any_launch(const GluGemm& a, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// Rows on 16-byte boundaries: BM x BN sums per workgroup of WM x WN waves,
+// Rows on 4-byte boundaries (16-byte ones fastest): BM x BN sums per workgroup of WM x WN waves,
 // pieces of both operands moved from memory into LDS directly, 64 of the summed
 // axis a stage and NS stages in a ring.  A wave holds its fragments of the next
 // 32 in registers while the matrix instructions take the current ones, so that
@@ -275,7 +298,7 @@ hipError_t any_launch(const GluGemm& a, hipStream_t stream) {
 // reads.  Forward: b's tile holds, for each wave's 64 columns, 32 rows of gate and
 // the same 32 of up, so that a lane ends with 8 columns of both.
 // ---------------------------------------------------------------------------
-template <GluOp OP, int FMT, int BM, int BN, int WM, int WN, int NS, bool PAST>
+template <GluOp OP, int FMT, int BM, int BN, int WM, int WN, int NS, bool PAST, bool THROUGH>
 __global__ __launch_bounds__(WM* WN * 64, NS*(BM + BN) * 128 > 81920 && WM * WN == 4 ? 1 : 2) void glu_tile(const GluGemm a, uint32_t tiles_m, uint32_t tiles_n) {
   constexpr bool kForward = OP == GluOp::kForward, kInput = OP == GluOp::kInput, kWeight = OP == GluOp::kWeight;
   constexpr bool kARow = !kWeight, kBRow = kForward;
@@ -350,10 +373,50 @@ __global__ __launch_bounds__(WM* WN * 64, NS*(BM + BN) * 128 > 81920 && WM * WN 
   // Forward: this wave's loads of b are all of gate or all of up.
   const int up = kForward ? wave * kBLoads / kUpAt % 2 : 0;
   const Rsrc rb_row = make_rsrc((const char*)a.b[up] + n0 * a.ldb * 2, cols_b, K * 2, pitch_b);
+  // THROUGH: rows at any address, in registers on their way: what a thread's loads would have put into LDS
+  u32x4 ta[THROUGH ? kALoads : 1], tb[THROUGH ? kBLoads : 1];
+  auto fetch_a = [&](int stage, int j) {
+    const int t = wave * kALoads + j;
+    const bool live = stage < stages;
+    if constexpr (kARow) {
+      const int64_t m = m0 + t * 8 + (lane >> 3);
+      ta[j] = ld_piece<2>(a_of(stage) + m * a.lda * 2, k_of(stage) * 2 + ((lane & 7) ^ (lane >> 3)) * 16, a.K * 2, live && m < a.M);
+    } else {
+      const int row = t * kARows + lane / kAPer;
+      const int64_t k = k_of(stage) + row;
+      ta[j] = ld_piece<2>(a_of(stage) + k * a.lda * 2, m0 * 2 + ((lane % kAPer) ^ s_of(row)) * 16, a.M * 2, live && k < a.K);
+    }
+  };
+  auto fetch_b = [&](int stage, int j) {
+    const int t = wave * kBLoads + j;
+    const bool live = stage < stages;
+    if constexpr (kBRow) {
+      const int64_t n = n0 + t / (2 * kUpAt) * (TN / 2) + t % kUpAt * 8 + (lane >> 3);
+      tb[j] = ld_piece<2>((const char*)a.b[up] + n * a.ldb * 2,
+                          k_of(stage) * 2 + ((lane & 7) ^ (kNarrow ? lane >> 3 : (lane >> 3 & 3) | (t & 1) << 2)) * 16, a.K * 2, live && n < a.N);
+    } else {
+      const int row = t * kBRows + lane / kBPer;
+      const int64_t k = k_of(stage) + row;
+      tb[j] = ld_piece<2>(b_of(stage) + k * a.ldb * 2, n0 * 2 + ((lane % kBPer) ^ s_of(row)) * 16, a.N * 2, live && k < a.K);
+    }
+  };
+  auto put_a = [&](int stage, int j) {
+    const int t = wave * kALoads + j;
+    const int at = kARow ? t * 1024 : t * kARows / 8 * kAGroup + t * kARows % 8 * BM * 2;
+    *(LDS u32x4*)((LDS char*)lds + (stage & (NS - 1)) * kBuf + at + lane * 16) = ta[j];
+  };
+  auto put_b = [&](int stage, int j) {
+    const int t = wave * kBLoads + j;
+    const int at = kBRow ? t * 1024 : t * kBRows / 8 * kBGroup + t * kBRows % 8 * BN * 2;
+    *(LDS u32x4*)((LDS char*)lds + (stage & (NS - 1)) * kBuf + kABytes + at + lane * 16) = tb[j];
+  };
   auto load_a = [&](int stage, int j) {
     const int t = wave * kALoads + j;
     const uint32_t to = lds0 + (stage & (NS - 1)) * kBuf;
-    if constexpr (kARow) {
+    if constexpr (THROUGH) {  // what was fetched for the stage, and its place is fetched again for the one after it
+      put_a(stage, j);
+      fetch_a(stage + 1, j);
+    } else if constexpr (kARow) {
       const Rsrc r = make_rsrc(a_of(stage) + m0 * a.lda * 2, rows_a, K * 2, pitch_a);
       load_to_lds(r, va_row + (uint32_t)(t * 8) * (uint32_t)pitch_a + from(stage), to + t * 1024);
     } else {
@@ -365,7 +428,10 @@ __global__ __launch_bounds__(WM* WN * 64, NS*(BM + BN) * 128 > 81920 && WM * WN 
   auto load_b = [&](int stage, int j) {
     const int t = wave * kBLoads + j;
     const uint32_t to = lds0 + (stage & (NS - 1)) * kBuf + kABytes;
-    if constexpr (kBRow) {
+    if constexpr (THROUGH) {
+      put_b(stage, j);
+      fetch_b(stage + 1, j);
+    } else if constexpr (kBRow) {
       const int row = t / (2 * kUpAt) * (TN / 2) + t % kUpAt * 8;  // of gate or up
       load_to_lds(rb_row, vb_row[t & 1] + (uint32_t)row * (uint32_t)pitch_b + from(stage), to + t * 1024);
     } else {
@@ -461,6 +527,12 @@ __global__ __launch_bounds__(WM* WN * 64, NS*(BM + BN) * 128 > 81920 && WM * WN 
   };
   // The ring: stage s lies in buffer s % NS; stage s + NS is loaded into it once every wave has read the last of s.
   if (stages > 0) {
+    if constexpr (THROUGH) {
+#pragma unroll
+      for (int j = 0; j < kALoads; ++j) fetch_a(0, j);
+#pragma unroll
+      for (int j = 0; j < kBLoads; ++j) fetch_b(0, j);
+    }
 #pragma unroll
     for (int p = 0; p < NS; ++p) {
 #pragma unroll
@@ -468,14 +540,15 @@ __global__ __launch_bounds__(WM* WN * 64, NS*(BM + BN) * 128 > 81920 && WM * WN 
 #pragma unroll
       for (int j = 0; j < kBLoads; ++j) load_b(p, j);
     }
-    meet<(NS - 1) * kLoads>();
+    // (THROUGH: the compiler waits for what a put needs; all puts are done where the waves meet)
+    meet < THROUGH ? 63 : (NS - 1) * kLoads > ();
 #pragma unroll
     for (int j = 0; j < FN; ++j) read_b(0, 0, j);
 #pragma unroll
     for (int i = 0; i < FM; ++i) read_a(0, 0, i);
     for (int s = 0; s < stages; ++s) {
       half_step(First{}, s);
-      meet<(NS - 2) * kLoads>();  // all but the stages after the next have landed
+      meet < THROUGH ? 63 : (NS - 2) * kLoads > ();  // all but the stages after the next have landed
       half_step(Second{}, s);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way to LDS when the workgroup ends
@@ -518,20 +591,20 @@ __global__ __launch_bounds__(WM* WN * 64, NS*(BM + BN) * 128 > 81920 && WM * WN 
   }
 }
 
-template <GluOp OP, int FMT, int BM, int BN, int WM, int WN, int NS>
+template <GluOp OP, int FMT, int BM, int BN, int WM, int WN, int NS, bool THROUGH = false>
 hipError_t tile_launch(const GluGemm& a, hipStream_t stream) {
   constexpr int kOutN = OP == GluOp::kForward ? BN / 2 : BN;
   const uint32_t tm = (uint32_t)((a.M + BM - 1) / BM), tn = (uint32_t)((a.N + kOutN - 1) / kOutN);
   const dim3 grid(tm * tn, OP == GluOp::kWeight ? 2 : 1);
-  if constexpr (BM >= 128 && OP != GluOp::kWeight) {
+  if constexpr (BM >= 128 && OP != GluOp::kWeight && !THROUGH) {
     bool whole = true;  // 16-bit outputs in whole pieces of 64 bytes
     for (int p = 0; p < 3; ++p) whole = whole && (a.out[p] == nullptr || ((uintptr_t)a.out[p] | (uintptr_t)(a.ldo[p] * 2)) % 64 == 0);
     if (whole) {
-      glu_tile<OP, FMT, BM, BN, WM, WN, NS, true><<<grid, WM * WN * 64, 0, stream>>>(a, tm, tn);
+      glu_tile<OP, FMT, BM, BN, WM, WN, NS, true, THROUGH><<<grid, WM * WN * 64, 0, stream>>>(a, tm, tn);
       return hipGetLastError();
     }
   }
-  glu_tile<OP, FMT, BM, BN, WM, WN, NS, false><<<grid, WM * WN * 64, 0, stream>>>(a, tm, tn);
+  glu_tile<OP, FMT, BM, BN, WM, WN, NS, false, THROUGH><<<grid, WM * WN * 64, 0, stream>>>(a, tm, tn);
   return hipGetLastError();
 }
 
@@ -697,16 +770,15 @@ hipError_t input_split_launch(const GluGemm& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Rows that the tiled kernels take: on 16-byte boundaries (a single row at any
-// distance from the next), offsets within a tile below 2^31, a grid that a
-// launch can hold.
-bool rows16(const void* p, int64_t rows, int64_t ld) {
-  return (uintptr_t)p % 16 == 0 && (rows <= 1 || (ld % 8 == 0 && ld <= (1 << 21)));
+// Rows that the direct loads take: on 4-byte boundaries (a single row at any
+// distance from the next), offsets within a tile below 2^31.
+bool rows4(const void* p, int64_t rows, int64_t ld) {
+  return (uintptr_t)p % 4 == 0 && (rows <= 1 || (ld % 2 == 0 && ld <= (1 << 21)));
 }
 int64_t tiles_of(const GluGemm& a, int64_t bm, int64_t bn) { return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn); }
 constexpr int64_t kMostTiles = 1 << 22;
 
-// The kernel of a product with 16-byte rows, by the time it takes: a start, and so much a stage of 64 of the summed axis,
+// The kernel of a product with rows on 4-byte boundaries, by the time it takes: a start, and so much a stage of 64 of the summed axis,
 // between `few` for a few workgroups and `full` for as many as run at once; more go in rounds (half overlapped) with a
 // start of their own.  us, fitted to 54 shapes from 1 to 9683 tokens on 256 compute units, inputs from memory: off by 6 to
 // 20%, and what it picks is 1.0 to 1.8% behind the best kernel's time in the mean.  For example, forward: 1 x 1024 x 1024 4.9 by
@@ -754,11 +826,16 @@ hipError_t gemm_launch(const GluGemm& given, hipStream_t stream) {
   GluGemm a = given;
   const bool weight = OP == GluOp::kWeight, forward = OP == GluOp::kForward;
   const int64_t rows_a = weight ? a.K : a.M, rows_b = forward ? a.N : a.K;
-  bool fast = a.K > 0 && tiles_of(a, 64, 32) < kMostTiles && rows16(a.a[0], rows_a, a.lda) && rows16(a.b[0], rows_b, a.ldb);
-  if (!forward) fast = fast && rows16(a.a[1], rows_a, a.lda);
-  if (!weight) fast = fast && rows16(a.b[1], rows_b, a.ldb);
+  bool fast = a.K > 0 && tiles_of(a, 64, 32) < kMostTiles && rows4(a.a[0], rows_a, a.lda) && rows4(a.b[0], rows_b, a.ldb);
+  if (!forward) fast = fast && rows4(a.a[1], rows_a, a.lda);
+  if (!weight) fast = fast && rows4(a.b[1], rows_b, a.ldb);
   if (!weight) fast = fast && a.K <= (1 << 21);  // (a single row may be longer)
-  if (!fast) return any_launch<OP, FMT>(a, stream);
+  const int64_t parts = weight ? 2 : 1;
+  if (!fast) {
+    const int64_t tiles = parts * tiles_of(a, 128, forward ? 64 : 128);
+    if (a.K == 0 || tiles < 64 || tiles >= kMostTiles) return any_launch<OP, FMT>(a, stream);
+    return tile_launch<OP, FMT, 128, 128, 2, 2, 2, true>(a, stream);
+  }
   // a single row: any distance that holds what a tile reads of it
   const int64_t wide_a = weight ? 256 : a.K, wide_b = forward ? a.K : 256;
   if (rows_a <= 1) a.lda = (wide_a + 255) / 256 * 256;

@@ -63,18 +63,12 @@ def near(got, want, kind, sums=0.0):
     return True
 
 
-# (gap, lead) of every matrix: rows on 16-byte boundaries, and rows anywhere
-LAYOUTS = [(0, 0), (8, 16), (5, 3)]
+# (gap, lead) of every matrix: rows on 16-byte boundaries, on 4-byte ones (where the columns are even), and anywhere
+LAYOUTS = [(0, 0), (8, 16), (6, 2), (5, 3)]
 SHAPES = [(1, 1, 1), (1, 8, 8), (1, 300, 520), (3, 7, 5), (2, 33, 64), (16, 64, 128), (17, 130, 72), (64, 32, 64), (65, 96, 200),
           (100, 264, 136), (129, 257, 65), (300, 200, 328)]
 # tiles of 128 and of 256, ragged at every side, and a summed axis that ends inside a stage
 LARGE = [(520, 1400, 200), (700, 2100, 1000), (2100, 2600, 136), (2304, 3600, 72)]
-
-
-def layouts(shape):
-    for gap, lead in LAYOUTS:
-        pad = -shape[1] % 8 if gap != 5 else 0
-        yield gap, lead, pad
 
 
 def buf(rows, cols, dtype, gap, lead, values=None):
