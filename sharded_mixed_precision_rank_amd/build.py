@@ -9,7 +9,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libzshard.so")
 # Device code and HIP-runtime host code, compiled as HIP, one object a source.
 SOURCES = [os.path.join(CSRC, f) for f in ("zs_kernels.hip", "zs_twopass.hip", "zs_q8_rows.hip", "zs_q8_gemm.hip",
-                                           "zs_glu_rows.hip", "zs_glu_gemm.hip", "zs_muon.hip", "zs_api.cpp", "zs_offload.cpp",
+                                           "zs_glu_rows.hip", "zs_glu_gemm.hip", "zs_muon.hip", "zs_muon_small.hip", "zs_api.cpp", "zs_offload.cpp",
                                            "zs_q8.cpp", "zs_glu.cpp", "zs_muon.cpp")]
 # The host AdamW is plain C++ built by the host compiler into an object that
 # the hipcc link takes as is (its AVX2 path is chosen at run time).  Compiling

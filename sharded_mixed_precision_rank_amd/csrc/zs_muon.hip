@@ -17,38 +17,19 @@
 // Matrices lie in rows of groups of 128 bytes: 32 hi parts, then the 32 lo parts.
 // Rows and columns are padded with zeros to multiples of 32, which the products
 // keep at zero.
-#include "zs_muon.h"
-#include "zs_tile_dev.h"
+#include "zs_muon_dev.h"
 
 namespace zs {
 namespace {
 
 using namespace dev;
-
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-
-constexpr float kUnit = 4096.0f;           // held values are this times the matrix's
-constexpr float kPerUnit = 1.0f / 4096.0f;
-constexpr int kMostPartials = 1024;        // sums of squares of a matrix
-
-int64_t padded(int64_t n) { return (n + 31) / 32 * 32; }
+using namespace ns;
 
 // ---------------------------------------------------------------------------
 // The update's first pass: the replicas' mean (fixed order, one rounding an
 // operation), the momentum, and u, whose squares are summed in 64 bits, a
 // workgroup's part in its own place.  Bound by memory: 2 N + 12 bytes a value.
 // ---------------------------------------------------------------------------
-struct MeanArgs {
-  const uint16_t* g[ZS_MAX_REPLICAS];
-  float* momentum;
-  float* u;
-  double* partials;
-  int64_t n;  // values of a matrix
-  int32_t n_rep, nesterov;
-  float mu;
-};
-
 __device__ __forceinline__ double block_sum(double v, double* lds) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
@@ -57,12 +38,6 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   const double t = (lds[0] + lds[1]) + (lds[2] + lds[3]);
   __syncthreads();
   return t;
-}
-
-__device__ __forceinline__ float mean_step(float s, float m, const MeanArgs& a, float& m1) {
-  const float g = s / (float)a.n_rep;
-  m1 = a.mu * m + g;
-  return a.nesterov ? g + a.mu * m1 : m1;
 }
 
 __global__ __launch_bounds__(256) void ns_mean(const MeanArgs a) {
@@ -112,23 +87,6 @@ struct NormArgs {
   double* partials;
 };
 template <int FMT>
-__device__ __forceinline__ void load8(const void* x, int64_t i, int64_t left, float (&v)[8]) {
-  if (left >= 8) {
-    if constexpr (FMT == kFP32) {
-      const f32x4 a = ld_any<f32x4>((const float*)x + i), b = ld_any<f32x4>((const float*)x + i + 4);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = a[k], v[4 + k] = b[k];
-    } else {
-      const u32x4 w = ld_any<u32x4>((const uint16_t*)x + i);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[2 * k] = h_lo<FMT>(w[k]), v[2 * k + 1] = h_hi<FMT>(w[k]);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = k < left ? ld_elem<FMT>(x, i + k) : 0.0f;
-  }
-}
-template <int FMT>
 __global__ __launch_bounds__(256) void ns_norm(const NormArgs a) {
   __shared__ double lds[4];
   const uint32_t per = (uint32_t)((a.cols + 7) / 8);
@@ -164,34 +122,6 @@ struct PackArgs {
   uint32_t* counters;            // zeroed here
   int32_t n_counters;            // of a matrix
 };
-
-__device__ __forceinline__ void to_parts(const float* t, u32x4& hi, u32x4& lo) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const _Float16 a = (_Float16)rounded(t[2 * k]), b = (_Float16)rounded(t[2 * k + 1]);
-    const _Float16 c = (_Float16)rounded(t[2 * k] - (float)a), d = (_Float16)rounded(t[2 * k + 1] - (float)b);
-    hi[k] = __builtin_bit_cast(uint32_t, (f16x2){a, b});
-    lo[k] = __builtin_bit_cast(uint32_t, (f16x2){c, d});
-  }
-}
-// Eight held values from column col (a multiple of 8) of a row of parts.
-__device__ __forceinline__ int64_t part_at(int64_t col) { return col / 32 * 128 + col % 32 * 2; }
-__device__ __forceinline__ void store_parts(char* row, int64_t col, const float* t) {
-  u32x4 hi, lo;
-  to_parts(t, hi, lo);
-  GLB char* p = (GLB char*)row + part_at(col);
-  *(GLB u32x4*)p = hi;
-  *(GLB u32x4*)(p + 64) = lo;
-}
-__device__ __forceinline__ void load_parts(const char* row, int64_t col, float* t) {
-  const GLB char* p = (const GLB char*)row + part_at(col);
-  const u32x4 hi = *(const GLB u32x4*)p, lo = *(const GLB u32x4*)(p + 64);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    t[2 * k] = h_lo<kFP16>(hi[k]) + h_lo<kFP16>(lo[k]);
-    t[2 * k + 1] = h_hi<kFP16>(hi[k]) + h_hi<kFP16>(lo[k]);
-  }
-}
 
 template <int FMT>
 __global__ __launch_bounds__(256) void ns_pack(const PackArgs a) {
@@ -270,66 +200,8 @@ struct NsGemm {
   float* sums;        // of split tiles
   uint32_t* counters;
   int32_t n_counters;
-  // the last step
-  int32_t turned, update;
-  int64_t rows, cols;  // of the user's matrix
-  void* out;
-  int32_t out_format;
-  int64_t ld_out, batch_out;
-  float* master;
-  uint16_t* param;
-  float dk, ss;
+  NsLast last;
 };
-
-// Eight held values of the last X, at row `row` from column `col` of the user's matrix.
-template <int FMT>
-__device__ __forceinline__ void store_values(const NsGemm& a, int64_t row, int64_t col, const float* t) {
-  const int64_t i = (int64_t)blockIdx.y * a.batch_out + row * a.ld_out + col;
-  float v[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = t[k] * kPerUnit;
-  if (col + 8 <= a.cols) {
-    st_four<FMT>(a.out, i, v);
-    st_four<FMT>(a.out, i + 4, v + 4);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (col + k < a.cols) st_elem<FMT>(a.out, i + k, v[k]);
-  }
-}
-__device__ __forceinline__ void store_update(const NsGemm& a, int64_t row, int64_t col, const float* t) {
-  const int64_t i = (int64_t)blockIdx.y * a.batch_out + row * a.ld_out + col;
-  if (col + 8 <= a.cols) {
-#pragma unroll
-    for (int q = 0; q < 8; q += 4) {
-      const f32x4 p = ld_any<f32x4>(a.master + i + q);
-      float v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = a.dk * p[k] - a.ss * (t[q + k] * kPerUnit);
-      st_four<kFP32>(a.master, i + q, v);
-      st_four<kBF16>(a.param, i + q, v);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (col + k >= a.cols) continue;
-      const float v = a.dk * ((const GLB float*)a.master)[i + k] - a.ss * (t[k] * kPerUnit);
-      st_elem<kFP32>(a.master, i + k, v);
-      st_elem<kBF16>(a.param, i + k, v);
-    }
-  }
-}
-__device__ __forceinline__ void store_last(const NsGemm& a, int64_t row, int64_t col, const float* t) {
-  if (row >= a.rows || col >= a.cols) return;
-  if (a.update)
-    store_update(a, row, col, t);
-  else if (a.out_format == ZS_FORMAT_FP32)
-    store_values<kFP32>(a, row, col, t);
-  else if (a.out_format == ZS_FORMAT_BF16)
-    store_values<kBF16>(a, row, col, t);
-  else
-    store_values<kFP16>(a, row, col, t);
-}
 
 // Tile `id` of a triangle of tiles, row by row.
 __device__ __forceinline__ void triangle(uint32_t id, uint32_t& i, uint32_t& j) {
@@ -338,10 +210,6 @@ __device__ __forceinline__ void triangle(uint32_t id, uint32_t& i, uint32_t& j) 
   while ((r + 1) * (r + 2) / 2 <= id) ++r;
   i = r;
   j = id - r * (r + 1) / 2;
-}
-
-__device__ __forceinline__ f32x4 mfma_f16(i32x4 b, i32x4 a, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
 }
 
 template <NsOp OP, int BM, int BN, int WM, int WN, int NS>
@@ -555,8 +423,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ns_tile(const NsGemm a, uint32
   // Results, 8 consecutive columns a lane.  Symmetric ones go to their mirrored place too, and the last step of a taller
   // matrix only there: through LDS, a part of it for each wave.
   const bool final_step = a.d == nullptr;
-  const bool direct = !final_step || !a.turned;
-  const bool mirrored = kTurned ? final_step && a.turned : tm != tn;
+  const bool direct = !final_step || !a.last.turned;
+  const bool mirrored = kTurned ? final_step && a.last.turned : tm != tn;
   char* const d = a.d + (int64_t)blockIdx.y * a.batch_d;
   const char* const add = OP == NsOp::kGram ? nullptr : a.add + (int64_t)blockIdx.y * a.batch_d;
   LDS float* const turn = (LDS float*)((LDS char*)lds + wave * kTurn);
@@ -594,7 +462,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ns_tile(const NsGemm a, uint32
         }
         if (direct && live) {
           if (final_step)
-            store_last(a, m, n, t);
+            store_last(a.last, blockIdx.y, m, n, t);
           else
             store_parts(d + m * a.pitch_d, n, t);
         }
@@ -617,7 +485,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ns_tile(const NsGemm a, uint32
         const int64_t row = n0 + wn + r, col = m0 + wm + h * CM + c;
         if (row >= a.N || col >= a.M) continue;
         if (final_step)
-          store_last(a, row, col, t);
+          store_last(a.last, blockIdx.y, row, col, t);
         else
           store_parts(d + row * a.pitch_d, col, t);
       }
@@ -750,6 +618,7 @@ size_t ns_workspace_bytes(int64_t rows, int64_t cols, int64_t batch) {
 }
 
 hipError_t launch_ns(const NsProblem& p, void* workspace, hipStream_t stream) {
+  if (p.rows <= kSmallSide && p.cols <= kSmallSide) return launch_ns_small(p, stream);
   const NsLayout l = layout_of(p.rows, p.cols, p.batch);
   char* const ws = (char*)(((uintptr_t)workspace + 255) / 256 * 256);
   const int64_t n = p.rows * p.cols;
@@ -761,15 +630,9 @@ hipError_t launch_ns(const NsProblem& p, void* workspace, hipStream_t stream) {
   k.rows = p.rows;
   k.cols = p.cols;
   if (p.update) {
-    MeanArgs a{};
-    for (int r = 0; r < p.n_rep; ++r) a.g[r] = p.grads[r];
-    a.momentum = p.momentum;
+    MeanArgs a = mean_of(p);
     a.u = (float*)(ws + l.at_x[1]);  // until the first product writes there
     a.partials = partials;
-    a.n = n;
-    a.n_rep = p.n_rep;
-    a.nesterov = p.nesterov;
-    a.mu = p.mu;
     ns_mean<<<first_grid, 256, 0, stream>>>(a);
     k.x = a.u;
     k.ld = p.cols;
@@ -845,18 +708,7 @@ hipError_t launch_ns(const NsProblem& p, void* workspace, hipStream_t stream) {
     a.by_sum = 1.0f;
     if (s == p.steps - 1) {
       a.d = nullptr;
-      a.turned = p.rows > p.cols;
-      a.update = p.update;
-      a.rows = p.rows;
-      a.cols = p.cols;
-      a.out = p.out;
-      a.out_format = p.out_format;
-      a.ld_out = p.update ? p.cols : p.ld_out;
-      a.batch_out = p.update ? n : p.batch_out;
-      a.master = p.master;
-      a.param = p.param;
-      a.dk = p.dk;
-      a.ss = p.ss;
+      a.last = last_of(p);
     }
     if ((e = gemm_launch<NsOp::kApply>(a, l.apply, p.batch, stream)) != hipSuccess) return e;
   }
