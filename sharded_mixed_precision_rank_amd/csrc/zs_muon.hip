@@ -690,6 +690,12 @@ hipError_t launch_ns(const NsProblem& p, void* workspace, hipStream_t stream) {
     a.K = l.n;
     a.by_sum = 1.0f;
     if ((e = gemm_launch<NsOp::kGram>(a, l.gram, p.batch, stream)) != hipSuccess) return e;
+    if (l.m <= kSlabSide) {
+      NsSlab b{s_at, x, s == p.steps - 1 ? nullptr : ws + l.at_x[(s + 1) % 2], pitch_x, l.m * pitch_s, l.m * pitch_x, (int32_t)l.m, l.n,
+               p.coefs[3 * s], p.coefs[3 * s + 1], p.coefs[3 * s + 2], last_of(p)};
+      if ((e = launch_ns_slab(b, p.batch, stream)) != hipSuccess) return e;
+      continue;
+    }
     a.a = a.b = a.add = s_at;
     a.pitch_a = a.pitch_b = pitch_s;
     a.batch_a = a.batch_b = l.m * pitch_s;

@@ -52,13 +52,16 @@ __device__ __forceinline__ void load8(const void* x, int64_t i, int64_t left, fl
     for (int k = 0; k < 8; ++k) v[k] = k < left ? ld_elem<FMT>(x, i + k) : 0.0f;
   }
 }
+// Eight values as their parts.  (A product that the compiler folds into the conversion to hi is no matter: lo is what is
+// left of the fp32 value.)
 __device__ __forceinline__ void to_parts(const float* t, u32x4& hi, u32x4& lo) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const _Float16 a = (_Float16)rounded(t[2 * k]), b = (_Float16)rounded(t[2 * k + 1]);
-    const _Float16 c = (_Float16)rounded(t[2 * k] - (float)a), d = (_Float16)rounded(t[2 * k + 1] - (float)b);
-    hi[k] = __builtin_bit_cast(uint32_t, (f16x2){a, b});
-    lo[k] = __builtin_bit_cast(uint32_t, (f16x2){c, d});
+    const f16x2 h = __builtin_convertvector((f32x2){t[2 * k], t[2 * k + 1]}, f16x2);
+    const f32x2 back = __builtin_convertvector(h, f32x2);
+    const f16x2 l = __builtin_convertvector((f32x2){t[2 * k] - back[0], t[2 * k + 1] - back[1]}, f16x2);
+    hi[k] = __builtin_bit_cast(uint32_t, h);
+    lo[k] = __builtin_bit_cast(uint32_t, l);
   }
 }
 // Eight held values from column col (a multiple of 8) of a row of parts.
@@ -188,6 +191,19 @@ inline MeanArgs mean_of(const NsProblem& p) {
   a.mu = p.mu;
   return a;
 }
+
+// The rest of a step of a matrix with at most kSlabSide rows, from its S (zs_muon_small.hip).
+constexpr int64_t kSlabSide = 64;
+struct NsSlab {
+  const char *s, *x;
+  char* to;  // NULL: the last step
+  int64_t pitch_x, batch_s, batch_x;
+  int32_t m;
+  int64_t n;  // padded
+  float ca, cb, cc;
+  NsLast last;
+};
+hipError_t launch_ns_slab(const NsSlab& a, int64_t batch, hipStream_t stream);
 
 }  // namespace ns
 }  // namespace zs

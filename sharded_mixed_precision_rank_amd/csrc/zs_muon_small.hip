@@ -32,54 +32,66 @@ template <int SIDE>
 struct Small {
   static constexpr int kPitch = SIDE * 4, kBytes = SIDE * kPitch;
   static constexpr int WM = 2, WN = SIDE / 32, kThreads = WM * WN * 64;
-  static constexpr int TM = SIDE / WM, FM = TM / 16, FN = 2;  // 32 columns a wave
-  static __device__ __forceinline__ int at(int row, int piece) { return row * kPitch + (piece ^ (row & 7)) * 16; }
+  static constexpr int TM = SIDE / WM, FM = TM / 16;  // rows of a wave, which has 32 columns
 };
+template <int COLS>
+__device__ __forceinline__ int small_at(int row, int piece) {
+  return row * (COLS * 4) + (piece ^ (row & 7)) * 16;
+}
 
-// acc += a b^T (TURNED: a b) over `groups` groups of 32 of the summed axis, for this wave's TM x 32 sums.
-template <int SIDE, bool TURNED>
-__device__ __forceinline__ void small_product(const LDS char* a, const LDS char* b, int groups, int wm, int wn,
-                                              f32x4 (&acc)[Small<SIDE>::FM][2]) {
-  typedef Small<SIDE> L;
+// acc = a b^T (TURNED: a b) over `groups` groups of 32 of the summed axis, for a wave's 16 FM x 32 sums; a has CA columns in
+// LDS, b CB.
+template <int CA, int CB, bool TURNED, int FM>
+__device__ __forceinline__ void small_product(const LDS char* a, const LDS char* b, int groups, int wm, int wn, f32x4 (&acc)[FM][2]) {
   const int lane = threadIdx.x & 63, g = lane >> 4, i16 = lane & 15;
 #pragma unroll
-  for (int i = 0; i < L::FM; ++i)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
+  // A lane's places: the xor of a place is of the lane alone, groups and fragments lie at fixed distances from it.
+  const LDS char *at_a[2], *at_b[2], *at_t[2][2][2];
+#pragma unroll
+  for (int part = 0; part < 2; ++part) {
+    at_a[part] = a + small_at<CA>(wm + i16, part * 4 + g);
+    at_b[part] = b + small_at<CB>(wn + i16, part * 4 + g);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int four = 0; four < 2; ++four)  // 8 rows (4 and 4) of the summed axis x 16 columns
+        at_t[part][j][four] = b + small_at<CB>(8 * g + (i16 >> 2) + 4 * four, part * 4 + j * 2 + (i16 >> 1 & 1)) + (i16 & 1) * 8 + wn * 4;
+  }
   for (int k = 0; k < groups; ++k) {
-    i32x4 fa[2][L::FM], fb[2][2];
+    i32x4 fa[2][FM], fb[2][2];
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
 #pragma unroll
-      for (int i = 0; i < L::FM; ++i) fa[part][i] = *(const LDS i32x4*)(a + L::at(wm + i * 16 + i16, k * 8 + part * 4 + g));
+      for (int i = 0; i < FM; ++i) fa[part][i] = *(const LDS i32x4*)(at_a[part] + i * 16 * CA * 4 + k * 128);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if constexpr (TURNED) {
-          // 8 rows (4 and 4) of the summed axis x 16 columns
-          const int row = k * 32 + 8 * g + (i16 >> 2), piece = wn / 32 * 8 + part * 4 + j * 2 + (i16 >> 1 & 1);
-          const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(LDS char*)(b + L::at(row, piece) + (i16 & 1) * 8));
-          const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(LDS char*)(b + L::at(row + 4, piece) + (i16 & 1) * 8));
+          const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(LDS char*)(at_t[part][j][0] + k * 32 * CB * 4));
+          const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(LDS char*)(at_t[part][j][1] + k * 32 * CB * 4));
           fb[part][j] = __builtin_bit_cast(i32x4, (i16x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
         } else {
-          fb[part][j] = *(const LDS i32x4*)(b + L::at(wn + j * 16 + i16, k * 8 + part * 4 + g));
+          fb[part][j] = *(const LDS i32x4*)(at_b[part] + j * 16 * CB * 4 + k * 128);
         }
       }
     }
 #pragma unroll
     for (int p = 0; p < 3; ++p)  // lo hi, hi hi, hi lo
 #pragma unroll
-      for (int i = 0; i < L::FM; ++i)
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = mfma_f16(fb[p == 2][j], fa[p == 0][i], acc[i][j]);
   }
 }
 
-// f(row, column of the first, the 8 sums) for this wave's sums.
-template <int SIDE, class F>
-__device__ __forceinline__ void small_each(int wm, int wn, const f32x4 (&acc)[Small<SIDE>::FM][2], F f) {
+// f(fragment, row, column of the first, 8 held values) for a wave's sums.
+template <int FM, class F>
+__device__ __forceinline__ void small_each(int wm, int wn, const f32x4 (&acc)[FM][2], F f) {
   const int lane = threadIdx.x & 63, g = lane >> 4, i16 = lane & 15;
 #pragma unroll
-  for (int i = 0; i < Small<SIDE>::FM; ++i) {
+  for (int i = 0; i < FM; ++i) {
     float t[8];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -91,23 +103,54 @@ __device__ __forceinline__ void small_each(int wm, int wn, const f32x4 (&acc)[Sm
     f(i, wm + i * 16 + i16, wn + eight_at(g), t);
   }
 }
-template <int SIDE>
 __device__ __forceinline__ int small_piece(int col) { return col / 32 * 8 + col % 32 / 8; }
-template <int SIDE>
+template <int COLS>
 __device__ __forceinline__ void small_put(LDS char* to, int row, int col, const float* t) {
   u32x4 hi, lo;
   to_parts(t, hi, lo);
-  *(LDS u32x4*)(to + Small<SIDE>::at(row, small_piece<SIDE>(col))) = hi;
-  *(LDS u32x4*)(to + Small<SIDE>::at(row, small_piece<SIDE>(col) + 4)) = lo;
+  *(LDS u32x4*)(to + small_at<COLS>(row, small_piece(col))) = hi;
+  *(LDS u32x4*)(to + small_at<COLS>(row, small_piece(col) + 4)) = lo;
 }
-template <int SIDE>
+template <int COLS>
 __device__ __forceinline__ void small_add(const LDS char* from, int row, int col, float by, float* t) {
-  const u32x4 hi = *(const LDS u32x4*)(from + Small<SIDE>::at(row, small_piece<SIDE>(col)));
-  const u32x4 lo = *(const LDS u32x4*)(from + Small<SIDE>::at(row, small_piece<SIDE>(col) + 4));
+  const u32x4 hi = *(const LDS u32x4*)(from + small_at<COLS>(row, small_piece(col)));
+  const u32x4 lo = *(const LDS u32x4*)(from + small_at<COLS>(row, small_piece(col) + 4));
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     t[2 * k] = by * (h_lo<kFP16>(hi[k]) + h_lo<kFP16>(lo[k])) + t[2 * k];
     t[2 * k + 1] = by * (h_hi<kFP16>(hi[k]) + h_hi<kFP16>(lo[k])) + t[2 * k + 1];
+  }
+}
+// b S + c S^2 of the S in LDS (m x m, padded), in its place; barriers in it.
+template <int SIDE>
+__device__ __forceinline__ void small_poly(LDS char* s, int m, int wm, int wn, float cb, float cc) {
+  typedef Small<SIDE> L;
+  const bool in_s = wm < m && wn < m;
+  f32x4 acc[L::FM][2];
+  float b[L::FM][8];
+  if (in_s) {
+    small_product<SIDE, SIDE, false>(s, s, m / 32, wm, wn, acc);
+    small_each(wm, wn, acc, [&](int i, int row, int col, const float* t) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) b[i][k] = cc * t[k];
+      small_add<SIDE>(s, row, col, cb, b[i]);
+    });
+  }
+  __syncthreads();  // S has been read
+  if (in_s) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < L::FM; ++i) small_put<SIDE>(s, wm + i * 16 + (lane & 15), wn + eight_at(lane >> 4), b[i]);
+  }
+  __syncthreads();
+}
+// The last step's values at (row, col .. col + 7) of X.
+__device__ __forceinline__ void small_last(const NsLast& a, int64_t batch, int64_t row, int64_t col, const float* t) {
+  if (!a.turned) {
+    store_last(a, batch, row, col, t);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) store_one(a, batch, col + k, row, t[k]);
   }
 }
 
@@ -186,9 +229,9 @@ __global__ __launch_bounds__(Small<SIDE>::kThreads) void ns_small(const SmallArg
 #pragma unroll
       for (int k = 0; k < 8; ++k) {  // one value each of 8 rows of X
         if (col + k >= cols) continue;
-        const int piece = small_piece<SIDE>(row);
-        *(LDS uint16_t*)(x + L::at(col + k, piece) + row % 8 * 2) = (uint16_t)(hi[k / 2] >> (k % 2 * 16));
-        *(LDS uint16_t*)(x + L::at(col + k, piece + 4) + row % 8 * 2) = (uint16_t)(lo[k / 2] >> (k % 2 * 16));
+        const int piece = small_piece(row);
+        *(LDS uint16_t*)(x + small_at<SIDE>(col + k, piece) + row % 8 * 2) = (uint16_t)(hi[k / 2] >> (k % 2 * 16));
+        *(LDS uint16_t*)(x + small_at<SIDE>(col + k, piece + 4) + row % 8 * 2) = (uint16_t)(lo[k / 2] >> (k % 2 * 16));
       }
     }
   }
@@ -199,29 +242,15 @@ __global__ __launch_bounds__(Small<SIDE>::kThreads) void ns_small(const SmallArg
   for (int step = 0; step < a.steps; ++step) {
     const float ca = a.coefs[3 * step], cb = a.coefs[3 * step + 1], cc = a.coefs[3 * step + 2];
     if (in_s) {
-      small_product<SIDE, false>(x, x, a.n / 32, wm, wn, acc);
-      small_each<SIDE>(wm, wn, acc, [&](int, int row, int col, const float* t) { small_put<SIDE>(s, row, col, t); });
+      small_product<SIDE, SIDE, false>(x, x, a.n / 32, wm, wn, acc);
+      small_each(wm, wn, acc, [&](int, int row, int col, const float* t) { small_put<SIDE>(s, row, col, t); });
     }
     __syncthreads();
+    small_poly<SIDE>(s, a.m, wm, wn, cb, cc);
     float b[L::FM][8];
-    if (in_s) {
-      small_product<SIDE, false>(s, s, a.m / 32, wm, wn, acc);
-      small_each<SIDE>(wm, wn, acc, [&](int i, int row, int col, const float* t) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) b[i][k] = cc * t[k];
-        small_add<SIDE>(s, row, col, cb, b[i]);
-      });
-    }
-    __syncthreads();  // S has been read
-    if (in_s) {
-      const int lane = tid & 63;
-#pragma unroll
-      for (int i = 0; i < L::FM; ++i) small_put<SIDE>(s, wm + i * 16 + (lane & 15), wn + eight_at(lane >> 4), b[i]);
-    }
-    __syncthreads();
     if (in_x) {
-      small_product<SIDE, true>(s, x, a.m / 32, wm, wn, acc);
-      small_each<SIDE>(wm, wn, acc, [&](int i, int row, int col, const float* t) {
+      small_product<SIDE, SIDE, true>(s, x, a.m / 32, wm, wn, acc);
+      small_each(wm, wn, acc, [&](int i, int row, int col, const float* t) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) b[i][k] = t[k];
         small_add<SIDE>(x, row, col, ca, b[i]);
@@ -231,15 +260,7 @@ __global__ __launch_bounds__(Small<SIDE>::kThreads) void ns_small(const SmallArg
     if (step == a.steps - 1) {
       if (!in_x) return;
 #pragma unroll
-      for (int i = 0; i < L::FM; ++i) {
-        const int row = wm + i * 16 + (lane & 15);
-        if (!a.last.turned) {
-          store_last(a.last, batch, row, col, b[i]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) store_one(a.last, batch, col + k, row, b[i][k]);
-        }
-      }
+      for (int i = 0; i < L::FM; ++i) small_last(a.last, batch, wm + i * 16 + (lane & 15), col, b[i]);
       return;
     }
     __syncthreads();  // X has been read
@@ -249,6 +270,54 @@ __global__ __launch_bounds__(Small<SIDE>::kThreads) void ns_small(const SmallArg
     }
     __syncthreads();
   }
+}
+
+// ---------------------------------------------------------------------------
+// A long matrix with a short side of at most 64: the polynomial and X' = a X + B X in
+// one kernel, instead of one each.  A workgroup has 64 columns of X; every one of
+// them makes B = b S + c S^2 for itself, in LDS.  64 x 4096: 6.4 us, where the two
+// kernels take 4.2 and 5 and a launch more.  (With 128 rows it took 12, as long as
+// the two, and longer where there are more workgroups than compute units.)
+// ---------------------------------------------------------------------------
+template <int SIDE>
+__global__ __launch_bounds__(Small<SIDE>::kThreads) void ns_slab(const NsSlab a) {
+  typedef Small<SIDE> L;
+  constexpr int kCols = 64, FM = 2;
+  static_assert(L::kThreads / 64 == SIDE / 32 * 2, "32 x 32 values a wave");
+  __shared__ __attribute__((aligned(1024))) char lds[L::kBytes + SIDE * kCols * 4];
+  LDS char* const s = (LDS char*)lds;
+  LDS char* const x = s + L::kBytes;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * kCols, batch = blockIdx.y;
+  const int m = a.m, cols = a.n - n0 < kCols ? (int)(a.n - n0) : kCols;  // multiples of 32
+  const char* const from_s = a.s + batch * a.batch_s;
+  const char* const from_x = a.x + batch * a.batch_x + n0 * 4;
+  for (int i = tid; i < m * (SIDE / 4); i += L::kThreads) {
+    const int row = i / (SIDE / 4), piece = i % (SIDE / 4);
+    if (piece * 4 < m)
+      *(LDS u32x4*)(s + small_at<SIDE>(row, piece)) = *(const GLB u32x4*)(const GLB char*)(from_s + (int64_t)row * (m * 4) + piece * 16);
+  }
+  for (int i = tid; i < m * (kCols / 4); i += L::kThreads) {
+    const int row = i / (kCols / 4), piece = i % (kCols / 4);
+    if (piece * 4 < cols)
+      *(LDS u32x4*)(x + small_at<kCols>(row, piece)) = *(const GLB u32x4*)(const GLB char*)(from_x + (int64_t)row * a.pitch_x + piece * 16);
+  }
+  __syncthreads();
+  small_poly<SIDE>(s, m, wave / L::WN * L::TM, wave % L::WN * 32, a.cb, a.cc);
+  const int wm = wave / 2 * 32, wn = wave % 2 * 32;
+  if (wm >= m || wn >= cols) return;
+  f32x4 acc[FM][2];
+  small_product<SIDE, kCols, true>(s, x, m / 32, wm, wn, acc);
+  small_each(wm, wn, acc, [&](int, int row, int col, const float* t) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = t[k];
+    small_add<kCols>(x, row, col, a.ca, v);
+    if (a.to != nullptr)
+      store_parts(a.to + batch * a.batch_x + (int64_t)row * a.pitch_x, n0 + col, v);
+    else
+      small_last(a.last, batch, row, n0 + col, v);
+  });
 }
 
 template <int SIDE>
@@ -278,6 +347,16 @@ hipError_t small_launch(const NsProblem& p, hipStream_t stream) {
 }
 
 }  // namespace
+
+namespace ns {
+
+hipError_t launch_ns_slab(const NsSlab& a, int64_t batch, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.n + 63) / 64), (unsigned)batch);
+  ns_slab<kSlabSide><<<grid, Small<kSlabSide>::kThreads, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace ns
 
 hipError_t launch_ns_small(const NsProblem& p, hipStream_t stream) {
   return p.rows <= 64 && p.cols <= 64 ? small_launch<64>(p, stream) : small_launch<kSmallSide>(p, stream);
