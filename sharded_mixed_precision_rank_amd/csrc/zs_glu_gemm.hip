@@ -322,6 +322,7 @@ __global__ __launch_bounds__(WM* WN * 64, NS*(BM + BN) * 128 > 81920 && WM * WN 
   const int out = kWeight ? (int)blockIdx.y : 0;
   uint32_t tm, tn;
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  tm = scalar(tm), tn = scalar(tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * kOutN;
   const int32_t K = (int32_t)a.K;
   const int nk = (int)(((int64_t)K + kStage - 1) / kStage), stages = kInput ? 2 * nk : nk;
@@ -372,6 +373,8 @@ __global__ __launch_bounds__(WM* WN * 64, NS*(BM + BN) * 128 > 81920 && WM * WN 
 
   // Forward: this wave's loads of b are all of gate or all of up.
   const int up = kForward ? wave * kBLoads / kUpAt % 2 : 0;
+  const Rsrc ra_row = make_rsrc(a0 + m0 * a.lda * 2, rows_a, K * 2, pitch_a);
+  const Rsrc ra_next = make_rsrc((const char*)a.a[kInput ? 1 : 0] + m0 * a.lda * 2, rows_a, K * 2, pitch_a);
   const Rsrc rb_row = make_rsrc((const char*)a.b[up] + n0 * a.ldb * 2, cols_b, K * 2, pitch_b);
   // THROUGH: rows at any address, in registers on their way: what a thread's loads would have put into LDS
   u32x4 ta[THROUGH ? kALoads : 1], tb[THROUGH ? kBLoads : 1];
@@ -417,7 +420,8 @@ __global__ __launch_bounds__(WM* WN * 64, NS*(BM + BN) * 128 > 81920 && WM * WN 
       put_a(stage, j);
       fetch_a(stage + 1, j);
     } else if constexpr (kARow) {
-      const Rsrc r = make_rsrc(a_of(stage) + m0 * a.lda * 2, rows_a, K * 2, pitch_a);
+      const bool next = kInput && stage >= nk;
+      const Rsrc r = {next ? ra_next[0] : ra_row[0], next ? ra_next[1] : ra_row[1], ra_row[2], ra_row[3]};
       load_to_lds(r, va_row + (uint32_t)(t * 8) * (uint32_t)pitch_a + from(stage), to + t * 1024);
     } else {
       const Rsrc r = make_rsrc(a_of(stage) + (k_of(stage) * a.lda + m0) * 2, rows_at(stage), rows_a * 2, pitch_a);
@@ -675,10 +679,10 @@ __global__ __launch_bounds__(W * 64, 2) void glu_few(const GluGemm a, uint32_t t
   store_gated<FMT, 4, false>(a, m0 + row, n0 + four, v[0], v[1]);
 }
 
-template <int FMT, int W>
+template <int FMT>
 hipError_t few_launch(const GluGemm& a, hipStream_t stream) {
   const uint32_t tn = (uint32_t)((a.N + 15) / 16), tm = (uint32_t)((a.M + 15) / 16);
-  glu_few<FMT, W><<<dim3(tm * tn), W * 64, 0, stream>>>(a, tn);
+  glu_few<FMT, 4><<<dim3(tm * tn), 256, 0, stream>>>(a, tn);
   return hipGetLastError();
 }
 
@@ -699,6 +703,7 @@ __global__ __launch_bounds__(512, 2) void glu_input_split(const GluGemm a, uint3
   const int g = lane >> 4, i16 = lane & 15;
   uint32_t tm, tn;
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  tm = scalar(tm), tn = scalar(tn);
   const int64_t m0 = (int64_t)tm * 16, n0 = (int64_t)tn * 64;
   const int32_t K = (int32_t)a.K, half = (K + 31) / 32, steps = 2 * half;
   const int32_t pitch_a = (int32_t)a.lda * 2, pitch_b = (int32_t)a.ldb * 2;
@@ -785,25 +790,24 @@ constexpr int64_t kMostTiles = 1 << 22;
 // kFew, 6.4 by k64x32, 7.8 by k64; 61 x 4096 x 4096 55 / 18.1 / 20.7, 27.2 by k128; 333 x 11008 x 4096 136 by k64, 96 by k128, 88 by k192,
 // 100 by k256; input gradient: 61 x 4096 x 4096 23.9 by kSplit, 37 by k32, 67 by k128; 1025 x 1376 x 4096 118 by kSplit, 56 by k128, 43 by
 // k128Near, 60 by k256; weight gradients: 61 x 4096 x 4096 25.7 by k64, 22.9 by k128Near, 20.4 by k256.
-enum class GluTile { kFew, kFew8, kSplit, k64x32, k32, k64, k64x128, k128, k128Near, k192, k256 };
+enum class GluTile { kFew, kSplit, k64x32, k32, k64, k64x128, k128, k128Near, k192, k256 };
 struct TileCost {
   GluTile tile;
   int bm, bn, at_once;  // sums of a workgroup; workgroups at once
   double start, few, full, round;
 };
 constexpr TileCost kForwardCosts[] = {{GluTile::kFew, 16, 32, 2048, 3.68, 0.089, 1.459, 0.0},
-                                      {GluTile::kFew8, 16, 32, 1024, 5.72, 0.088, 0.635, 5.45},
                                       {GluTile::k64x32, 64, 32, 256, 3.74, 0.200, 0.237, 1.24},
                                       {GluTile::k64, 64, 64, 512, 3.80, 0.243, 0.455, 0.40},
-                                      {GluTile::k128, 128, 128, 256, 4.07, 0.337, 0.521, 2.13},
-                                      {GluTile::k192, 192, 128, 512, 2.17, 0.700, 1.256, 1.61},
-                                      {GluTile::k256, 256, 256, 256, 3.42, 1.128, 1.525, 3.95}};
+                                      {GluTile::k128, 128, 128, 256, 4.50, 0.324, 0.516, 2.14},
+                                      {GluTile::k192, 192, 128, 512, 6.00, 0.564, 1.195, 2.32},
+                                      {GluTile::k256, 256, 256, 256, 7.00, 0.972, 1.518, 3.42}};
 constexpr TileCost kInputCosts[] = {{GluTile::kSplit, 16, 64, 256, 3.02, 0.124, 0.165, 1.30},
                                     {GluTile::k32, 32, 64, 512, 3.40, 0.248, 0.334, 0.72},
                                     {GluTile::k64x128, 64, 128, 256, 4.54, 0.356, 0.435, 1.48},
-                                    {GluTile::k128, 128, 128, 256, 4.18, 0.471, 0.612, 2.13},
-                                    {GluTile::k128Near, 128, 128, 512, 2.15, 0.722, 1.063, 1.60},
-                                    {GluTile::k256, 256, 256, 256, 3.96, 1.179, 1.622, 0.0}};
+                                    {GluTile::k128, 128, 128, 256, 5.00, 0.452, 0.603, 2.11},
+                                    {GluTile::k128Near, 128, 128, 512, 5.00, 0.647, 1.008, 2.00},
+                                    {GluTile::k256, 256, 256, 256, 7.00, 1.092, 1.548, 0.99}};
 constexpr TileCost kWeightCosts[] = {{GluTile::k64, 64, 64, 1024, 3.99, 0.294, 0.745, 2.01},
                                      {GluTile::k128, 128, 128, 256, 5.14, 0.406, 0.527, 2.55},
                                      {GluTile::k128Near, 128, 128, 512, 6.59, 0.460, 0.899, 3.05},
@@ -843,8 +847,7 @@ hipError_t gemm_launch(const GluGemm& given, hipStream_t stream) {
   const int64_t stages = (a.K + kStage - 1) / kStage;
   if constexpr (OP == GluOp::kForward) {
     switch (cheapest(kForwardCosts, a, 2 * a.N, 1, stages)) {
-      case GluTile::kFew: return few_launch<FMT, 4>(a, stream);
-      case GluTile::kFew8: return few_launch<FMT, 8>(a, stream);
+      case GluTile::kFew: return few_launch<FMT>(a, stream);
       case GluTile::k64x32: return tile_launch<OP, FMT, 64, 32, 4, 1, 8>(a, stream);
       case GluTile::k64: return tile_launch<OP, FMT, 64, 64, 4, 1, 4>(a, stream);
       case GluTile::k128: return tile_launch<OP, FMT, 128, 128, 4, 2, 4>(a, stream);

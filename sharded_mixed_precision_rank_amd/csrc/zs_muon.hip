@@ -243,6 +243,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ns_tile(const NsGemm a, uint32
     id = x * per + (x < more ? x : more) + bid / 8;
     triangle(id, tm, tn);
   }
+  tm = scalar(tm), tn = scalar(tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int all = (int)(a.K / 32);
   const int first = (int)((int64_t)all * split / (uint32_t)a.splits), last = (int)((int64_t)all * (split + 1) / (uint32_t)a.splits);

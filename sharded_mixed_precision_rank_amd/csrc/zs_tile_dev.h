@@ -110,6 +110,14 @@ __device__ __forceinline__ void tile_of(uint32_t bid, uint32_t tiles_m, uint32_t
   tn = in / height;
 }
 
+// A value that is the same in every lane, in a scalar register from here on: what descriptors are made of inside a loop
+// must not be read back from vector registers there (see load_to_lds).
+__device__ __forceinline__ uint32_t scalar(uint32_t v) {
+  uint32_t s = __builtin_amdgcn_readfirstlane(v);
+  asm volatile("" : "+s"(s));
+  return s;
+}
+
 // f of 0 .. N - 1, each a constant: unrolled whatever its size.
 template <class F, int... I>
 __device__ __forceinline__ void for_each(F f, std::integer_sequence<int, I...>) {

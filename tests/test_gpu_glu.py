@@ -71,13 +71,20 @@ SHAPES = [(1, 1, 1), (1, 8, 8), (1, 300, 520), (3, 7, 5), (2, 33, 64), (16, 64, 
 LARGE = [(520, 1400, 200), (700, 2100, 1000), (2100, 2600, 136), (2304, 3600, 72)]
 
 
+# one more for each kernel that the sizes above do not reach: forward in tiles of 64 x 32, 64 x 64, 128 x 128, 192 x 128 and
+# 256 x 256; input gradient in 32 x 64, 64 x 128 and 128 x 128 in two forms; weight gradients in 128 x 128 in two forms
+FORWARD_TILES = [(61, 3924, 322), (67, 2141, 194), (262, 3362, 346), (333, 5504, 200), (2700, 2300, 136)]
+INPUT_TILES = [(2301, 70, 65), (292, 3345, 193), (2298, 2870, 72), (3379, 533, 72)]
+WEIGHT_TILES = [(457, 3823, 326), (739, 2766, 33), (1600, 2300, 520)]
+
+
 def buf(rows, cols, dtype, gap, lead, values=None):
     """Rows whose distance is a multiple of 8 elements, unless the gap is odd."""
     return Buf(rows, cols, dtype, gap + (-cols % 8 if gap % 8 == 0 else 0), lead, values)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
-@pytest.mark.parametrize("shape", SHAPES + LARGE)
+@pytest.mark.parametrize("shape", SHAPES + LARGE + FORWARD_TILES)
 def test_forward_of_whole_numbers(zs, shape, kind):
     T, N, K = shape
     rng = np.random.default_rng(T * 31 + N * 7 + K)
@@ -99,7 +106,7 @@ def test_forward_of_whole_numbers(zs, shape, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
-@pytest.mark.parametrize("shape", SHAPES + LARGE)
+@pytest.mark.parametrize("shape", SHAPES + LARGE + INPUT_TILES)
 def test_input_grad_of_whole_numbers(zs, shape, kind):
     T, K, N = shape
     rng = np.random.default_rng(T * 31 + N * 7 + K)
@@ -116,7 +123,7 @@ def test_input_grad_of_whole_numbers(zs, shape, kind):
 
 @pytest.mark.parametrize("out", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
-@pytest.mark.parametrize("shape", SHAPES + LARGE)
+@pytest.mark.parametrize("shape", SHAPES + LARGE + WEIGHT_TILES)
 def test_weight_grad_of_whole_numbers(zs, shape, kind, out):
     N, K, T = shape
     rng = np.random.default_rng(T * 31 + N * 7 + K)
