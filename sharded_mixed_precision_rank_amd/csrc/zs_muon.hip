@@ -498,8 +498,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ns_tile(const NsGemm a, uint32
 // ---------------------------------------------------------------------------
 // The choice of tiles, and the workspace.
 // ---------------------------------------------------------------------------
-enum class NsTile : int32_t { k64 = 0, k128 = 1, k192 = 2, k256 = 3 };
-constexpr int kTileSide[4] = {64, 128, 192, 256};
+enum class NsTile : int32_t { k32 = 0, k64 = 1, k128 = 2, k192 = 3, k256 = 4 };
+constexpr int kTiles = 5, kTileSide[kTiles] = {32, 64, 128, 192, 256};
 struct Choice {
   NsTile tile;
   int32_t splits;
@@ -510,15 +510,19 @@ int64_t tiles_of(int64_t m, int64_t n, int64_t side, bool triangle) {
   return triangle ? tm * (tm + 1) / 2 : tm * tn;
 }
 // The tile and the split of a product, by the time its kernel takes (us, measured on 256 compute units): a start and an
-// end, and so much a stage of 32 for a few workgroups, for 256, and for 512 where two fit a unit; more go in rounds, which
-// overlap by half.  Split sums cost their exchange.  For example (rows x columns, product): 1024 x 1024, S: 10.8 in 64 x 64
-// tiles, 27 in 128 x 128, 64 in 256 x 256; 2048 x 2048, S 46 / 48 / 108, B X 62 / 55 / 108; 4096 x 4096, S 332 / 213 / 205, in 192
-// x 192 172, B X 419 / 305 / 275, in 192 x 192 328.  64 x 4096, S in 64 x 64 tiles: 26.6, in 2 splits 16.9, 8 10.1, 16 11.5.
+// end, and so much a stage of 32 for a few workgroups, for 256, and for 512 where two or more fit a unit; more go in
+// rounds, which overlap by half.  Split sums cost their exchange.  For example (rows x columns, product): 256 x 768, S 6.2
+// in 32 x 32 tiles, 8.1 in 64 x 64; 1024 x 1024, S 10.6 / 10.6, in 128 x 128 27, in 256 x 256 64, B X 16.2 / 13.2 / 29 / 62;
+// 2048 x 2048, S 46 in 64 x 64, 48 in 128 x 128, 108 in 256 x 256, B X 62 / 55 / 108; 4096 x 4096, S 332 / 213 / 205, in 192 x 192 172,
+// B X 419 / 305 / 275, in 192 x 192 328.  128 x 4096, S in 32 x 32 tiles: 20.0, in 2 splits 13.1, in 4 9.4.  (Small tiles are
+// bound by what a compute unit takes in, 94 bytes a ns alone and 58 with all: waves that split a workgroup's sums four ways
+// took as long, 9.2 against 7.6 us at 4 x 512 x 512.)
 struct TileTime {
   double start, few, full, twice;  // twice = 0: one a unit
   double exchange, exchange_each;
 };
-constexpr TileTime kTileTime[4] = {{4.0, 0.175, 0.29, 0.45, 2.8, 0.35},
+constexpr TileTime kTileTime[kTiles] = {{3.8, 0.12, 0.16, 0.22, 1.2, 0.25},
+                                        {4.0, 0.175, 0.29, 0.45, 2.0, 0.35},
                                    {5.5, 0.47, 0.78, 1.17, 4.0, 0.9},
                                    {7.0, 0.83, 1.33, 0.0, 8.0, 2.0},
                                    {10.0, 1.37, 2.1, 0.0, 12.0, 3.5}};
@@ -539,9 +543,9 @@ double product_us(int t, int64_t groups, int64_t stages, int64_t splits) {
 }
 Choice choose(int64_t m, int64_t n, int64_t k, int64_t batch, bool triangle) {
   const int64_t stages = k / 32;
-  Choice best{NsTile::k64, 1, 0};
+  Choice best{NsTile::k32, 1, 0};
   double least = 1e300;
-  for (int t = 0; t < 4; ++t) {
+  for (int t = 0; t < kTiles; ++t) {
     const int64_t tiles = tiles_of(m, n, kTileSide[t], triangle);
     for (int64_t splits = 1; splits <= 16; splits *= 2) {
       // split sums: of at most 512 workgroups, 4 stages each at least
@@ -604,6 +608,7 @@ hipError_t gemm_launch(const NsGemm& given, const Choice& c, int64_t batch, hipS
   const dim3 grid((unsigned)(c.tiles * c.splits), (unsigned)batch);
   const uint32_t tiles = (uint32_t)c.tiles;
   switch (c.tile) {
+    case NsTile::k32: ns_tile<OP, 32, 32, 2, 1, 4><<<grid, 128, 0, stream>>>(a, tm, tn, tiles); break;
     case NsTile::k64: ns_tile<OP, 64, 64, 2, 2, 4><<<grid, 256, 0, stream>>>(a, tm, tn, tiles); break;
     case NsTile::k128: ns_tile<OP, 128, 128, 2, 2, 2><<<grid, 256, 0, stream>>>(a, tm, tn, tiles); break;
     case NsTile::k192: ns_tile<OP, 192, 192, 4, 2, 2><<<grid, 512, 0, stream>>>(a, tm, tn, tiles); break;
