@@ -522,7 +522,7 @@ struct TileTime {
   double exchange, exchange_each;
 };
 constexpr TileTime kTileTime[kTiles] = {{3.8, 0.12, 0.16, 0.22, 1.2, 0.25},
-                                        {4.0, 0.175, 0.29, 0.45, 2.0, 0.35},
+                                        {4.0, 0.175, 0.29, 0.45, 2.4, 0.35},
                                    {5.5, 0.47, 0.78, 1.17, 4.0, 0.9},
                                    {7.0, 0.83, 1.33, 0.0, 8.0, 2.0},
                                    {10.0, 1.37, 2.1, 0.0, 12.0, 3.5}};
@@ -548,8 +548,9 @@ Choice choose(int64_t m, int64_t n, int64_t k, int64_t batch, bool triangle) {
   for (int t = 0; t < kTiles; ++t) {
     const int64_t tiles = tiles_of(m, n, kTileSide[t], triangle);
     for (int64_t splits = 1; splits <= 16; splits *= 2) {
-      // split sums: of at most 512 workgroups, 4 stages each at least
-      if (splits > 1 && (tiles * batch * splits > 512 || stages < 4 * splits)) break;
+      // split sums: of at most a workgroup a unit (1024 x 1024, S in 272 halves: 13.4 us, 10.6 in 136 whole ones), 4 stages
+      // each at least
+      if (splits > 1 && (tiles * batch * splits > 256 || stages < 4 * splits)) break;
       const double us = product_us(t, tiles * batch, stages, splits);
       if (us < least) {
         least = us;

@@ -104,6 +104,29 @@ def test_exact_products_of_large_matrices(zs, rows, cols):
         assert ((out.double() - want).abs() <= most).all()
 
 
+# the tiles of 128, 192 and 256 in each product, whole and with their sums split
+@pytest.mark.parametrize("batch,rows,cols", [(32, 96, 9664), (32, 192, 9504), (4, 992, 5344), (1, 2848, 2848), (8, 1344, 1344), (8, 1696, 1696),
+                                             (4, 160, 11424), (1, 5100, 5150)])
+def test_exact_products_of_stacks(zs, batch, rows, cols):
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    count = 4 ** int(math.log(rows * cols, 4) + 1e-9)
+    u = torch.zeros(batch, rows * cols, device="cuda")
+    for v in u:
+        at = torch.randperm(rows * cols, generator=gen, device="cuda")[:count]
+        v[at] = 2.0 * torch.randint(0, 2, (count,), generator=gen, device="cuda").float() - 1.0
+    u = u.view(batch, rows, cols)
+    ws = Guarded(zs, rows, cols, batch)
+    out = torch.empty_like(u)
+    for coefs in ((1.0, 1.0, 0.0), (1.0, 0.0, 1.0)):
+        out.fill_(math.nan)
+        zs.orthogonalize(u, out, ws.t, steps=1, coefs=coefs)
+        assert torch.isfinite(out).all()
+        for i in sorted({0, batch // 2, batch - 1}):
+            want, most = most_off(u[i], coefs)
+            assert ((out[i].double() - want).abs() <= most).all()
+    assert ws.untouched_outside()
+
+
 def off(got, want):
     """The error's 2-norm relative to an orthogonal matrix's."""
     return ((got.double() - want).norm() / min(want.shape) ** 0.5).item()
