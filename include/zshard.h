@@ -537,12 +537,17 @@ ZS_API zs_status zs_q8_weight_grad(const void* dy, int32_t dy_format, int64_t ld
  * rows in elements (at least the columns; not looked at for a single row); the
  * two weights share one, and so do gate and up, dgate and dup, and dw_gate,
  * dw_up and what is added to them.  A weight that holds gate and up one behind
- * the other is two matrices in one buffer.  Any alignment of the elements works;
- * rows that start on 16-byte boundaries (base and ld) run fastest.  Dimensions
- * are 0 .. 2^31 - 1; sums of nothing are zeros.  Which bytes outputs may share
- * and which bytes around the products' operands may be read is as for the 8-bit
- * operators above.  No workspace, no allocation; every call enqueues one kernel
- * on `stream` only and may be captured.  Results do not depend on what runs
+ * the other is two matrices in one buffer.  Any alignment of the elements works:
+ * rows that start on 16-byte boundaries (base and ld) run fastest, on 4-byte
+ * ones nearly as fast, others at about half the rate.  Dimensions are 0 .. 2^31 -
+ * 1; sums of nothing are zeros.  Which bytes outputs may share is as for the
+ * 8-bit operators above.  Of the products' operands whose rows start on 4-byte
+ * boundaries, the bytes between one row's end and the next row may be read too,
+ * and up to 3 bytes behind the last row, within its aligned 4-byte word; whatever
+ * they hold, and whatever is written to them meanwhile, reaches no result.
+ * Nothing else than the operands' rows and columns is read, and nothing but the
+ * outputs' own written.  No workspace, no allocation; every call enqueues one
+ * kernel on `stream` only and may be captured.  Results do not depend on what runs
  * beside them, call to call.
  *
  * Non-finite values spread as the formulas have it; a result past its format's
@@ -643,8 +648,8 @@ ZS_API size_t zs_orthogonalize_workspace_bytes(int64_t rows, int64_t cols, int64
 
 /* out = the Newton-Schulz steps of x, for each matrix of a batch.  x in x_format,
    out in out_format (BF16, FP16 or FP32): row-major, ld elements from row to row
-   and batch_stride elements from matrix to matrix, at least rows * ld (neither is
-   looked at where there is one).  Any alignment of the elements.  coefs as in
+   and batch_stride elements from matrix to matrix, which holds a whole one (neither
+   is looked at where there is one).  Any alignment of the elements.  coefs as in
    zs_muon_hp.  out may be x itself (same format, ld and batch stride).
    Errors: ZS_ERR_NULL, ZS_ERR_RANGE (also: workspace too small; coefficients not
    finite), ZS_ERR_ALIGN, ZS_ERR_ALIAS, ZS_ERR_HIP. */

@@ -1097,16 +1097,16 @@ class MuonHP:
 
 
 def _ns_workspace(workspace, rows, cols, batch, device, stream):
-    """The caller's workspace, or one of this call's own, whose reuse waits for ``stream``."""
+    """The caller's workspace, or one of this call's own, from the memory whose reuse follows ``stream``'s order."""
     if workspace is not None:
         _dev_check(workspace, _WORKSPACE_TYPES, "workspace")
         return workspace, workspace.numel() * workspace.element_size()
     n = orthogonalize_workspace_bytes(rows, cols, batch)
-    workspace = torch.empty(n, dtype=torch.uint8, device=device)
-    if stream is not None:
-        workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                                torch.cuda.ExternalStream(stream, device=device))
-    return workspace, n
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device), n
+    # (a block of the current stream's may still be in use there when `stream` writes it)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream):
+        return torch.empty(n, dtype=torch.uint8, device=device), n
 
 
 def _batched(t, formats, name):

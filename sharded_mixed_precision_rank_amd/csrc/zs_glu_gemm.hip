@@ -121,7 +121,7 @@ __device__ __forceinline__ i32x4 inside(int left) {
 }
 
 // ---------------------------------------------------------------------------
-// Rows at any address: 64 x 64 sums per workgroup of four waves (32 x 32 each),
+// Rows at any address, few tiles: 64 x 64 sums per workgroup of four waves (32 x 32 each),
 // operands staged through registers 16 bytes at a time, 64 of the summed axis a
 // stage, four stages ahead of the matrix instructions; two buffers in LDS and
 // one barrier a stage.  Forward: 32 columns of gate beside the same 32 of up.
@@ -284,13 +284,20 @@ hipError_t any_launch(const GluGemm& a, hipStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// Rows on 4-byte boundaries (16-byte ones fastest): BM x BN sums per workgroup of WM x WN waves,
-// pieces of both operands moved from memory into LDS directly, 64 of the summed
+// Rows on 4-byte boundaries (16-byte ones fastest): BM x BN sums per workgroup of WM x WN
+// waves, pieces of both operands moved from memory into LDS directly, 64 of the summed
 // axis a stage and NS stages in a ring.  A wave holds its fragments of the next
 // 32 in registers while the matrix instructions take the current ones, so that
 // LDS reads, memory loads and matrix instructions run side by side.  One barrier
 // a stage: between its halves every wave has read all of the stage and its part
-// of the next one has landed.
+// of the next one has landed.  THROUGH: rows at any address, which the direct loads
+// do not take, through registers (8192 x 11008 x 4096, rows one element off: 2180-2320 us).
+//
+// Bound, where there are many tiles, by the matrix instructions and the clock that they
+// leave: 8192 x 11008 x 4096 in bf16, 256 x 256 tiles, 1155-1257 us forward (1180-1280
+// TFLOP/s), 1110-1172 input gradient, 1122-1143 weight gradients, matrix pipes 66-74% busy at
+// 1.5-1.65 GHz; 32 x 32 x 16 instructions on the same fragments took 1221-1344 / 1169-1184 /
+// 1169.  With few tiles by what a compute unit takes in: 333 x 11008 x 4096 85 us in 192 x 128.
 //
 // An operand whose rows run along the summed axis lies in rows of 128 bytes,
 // read 16 bytes a lane; one whose rows lie across it (both weights in kInput,
@@ -601,7 +608,7 @@ hipError_t tile_launch(const GluGemm& a, hipStream_t stream) {
   const uint32_t tm = (uint32_t)((a.M + BM - 1) / BM), tn = (uint32_t)((a.N + kOutN - 1) / kOutN);
   const dim3 grid(tm * tn, OP == GluOp::kWeight ? 2 : 1);
   if constexpr (BM >= 128 && OP != GluOp::kWeight && !THROUGH) {
-    bool whole = true;  // 16-bit outputs in whole pieces of 64 bytes
+    bool whole = true;  // 16-bit outputs in whole pieces of 64 bytes: written past the caches, which keep the operands
     for (int p = 0; p < 3; ++p) whole = whole && (a.out[p] == nullptr || ((uintptr_t)a.out[p] | (uintptr_t)(a.ldo[p] * 2)) % 64 == 0);
     if (whole) {
       glu_tile<OP, FMT, BM, BN, WM, WN, NS, true, THROUGH><<<grid, WM * WN * 64, 0, stream>>>(a, tm, tn);

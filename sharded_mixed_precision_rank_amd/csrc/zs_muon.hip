@@ -28,7 +28,8 @@ using namespace ns;
 // ---------------------------------------------------------------------------
 // The update's first pass: the replicas' mean (fixed order, one rounding an
 // operation), the momentum, and u, whose squares are summed in 64 bits, a
-// workgroup's part in its own place.  Bound by memory: 2 N + 12 bytes a value.
+// workgroup's part in its own place.  Bound by memory: 2 N + 12 bytes a value (8
+// replicas of 11008 x 4096: 230 us, 5.5 TB/s).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ double block_sum(double v, double* lds) {
 #pragma unroll
@@ -185,6 +186,12 @@ __global__ __launch_bounds__(256) void ns_pack(const PackArgs a) {
 // Few tiles: the summed axis is split over `splits` workgroups.  Each leaves its
 // sums in the workspace; the last to arrive (a counter a tile) adds them in
 // their order, so the result does not depend on who that is.
+//
+// Large products are bound by the matrix instructions and the clock under them: 4096
+// x 4096, S and the polynomial 176 us each in 192 x 192 tiles (matrix pipes busy 65% at
+// 1.9 GHz), B X 290 in 256 x 256 (76% at 1.8 GHz; 1420 TFLOP/s of the parts' three
+// products); S of 4096 x 11008 449, B X 830.  Small ones by a launch's start and end, 4 us, and
+// what a compute unit takes in.
 // ---------------------------------------------------------------------------
 enum class NsOp : int32_t { kGram = 0, kPoly = 1, kApply = 2 };
 struct NsGemm {
@@ -523,9 +530,9 @@ struct TileTime {
 };
 constexpr TileTime kTileTime[kTiles] = {{3.8, 0.12, 0.16, 0.22, 1.2, 0.25},
                                         {4.0, 0.175, 0.29, 0.45, 2.4, 0.35},
-                                   {5.5, 0.47, 0.78, 1.17, 4.0, 0.9},
-                                   {7.0, 0.83, 1.33, 0.0, 8.0, 2.0},
-                                   {10.0, 1.37, 2.1, 0.0, 12.0, 3.5}};
+                                        {5.5, 0.47, 0.78, 1.17, 4.0, 0.9},
+                                        {7.0, 0.83, 1.33, 0.0, 8.0, 2.0},
+                                        {10.0, 1.37, 2.1, 0.0, 12.0, 3.5}};
 double product_us(int t, int64_t groups, int64_t stages, int64_t splits) {
   const TileTime& c = kTileTime[t];
   const int64_t all = groups * splits, at_once = c.twice > 0 ? 512 : 256;

@@ -3,9 +3,10 @@
 // values.  The products are those of zs_muon.hip (two fp16 parts an operand,
 // three products of them, fp32 sums).
 //
-// A batch of them is bound by the matrix instructions and LDS reads of a
-// workgroup, a single one by their latency: 15 products of 128 x 128 x 128 take
-// about 2 us each, where a kernel for each product takes 5-6.
+// Bound by a workgroup's LDS reads and the trips between them: 15 products of 128 x
+// 128 x 128, one behind the other, take 3.4 us each, whether one matrix or one for
+// every compute unit (32 of them, fp32 to bf16: 54 us, where a kernel for each
+// product took 96).  Reading fragments a group ahead was slower.
 #include "zs_muon_dev.h"
 
 namespace zs {

@@ -337,6 +337,24 @@ def test_other_stream_with_a_workspace_of_the_call(zs):
     assert all(torch.equal(o, want) for o, _ in outs)
 
 
+@pytest.mark.parametrize("handle", (False, True))
+def test_other_stream_beside_work_on_memory_just_freed(zs, handle):
+    """workspace=None on a stream that does not wait for the current one, whose queue still writes a block that was freed
+    there: the call's workspace is not that block."""
+    x = gradients(6, 300, 400)
+    want, out = torch.empty_like(x), torch.empty_like(x)
+    zs.orthogonalize(x, want)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    block = torch.empty(zs.orthogonalize_workspace_bytes(300, 400), dtype=torch.uint8, device="cuda")
+    for _ in range(400):
+        block.fill_(255)
+    del block
+    zs.orthogonalize(x, out, stream=side.cuda_stream if handle else side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
 def test_a_layers_training_steps(zs):
     """The gated block with the step of its weights, as a training loop has them: two replicas' forward and backward passes,
     their weight gradients as chunks, both weights (a stack of two) reduced, orthogonalised and updated, and the working
