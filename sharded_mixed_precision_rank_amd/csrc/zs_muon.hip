@@ -461,12 +461,11 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ns_tile(const NsGemm a, uint32
         }
         const int64_t n = n0 + wn + col;
         const bool live = m < a.M && n < a.N;
-        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (OP != NsOp::kGram && live) load_parts(add + m * a.pitch_d, n, x);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          t[r] = t[r] * (a.by_sum * kPerUnit);
-          if constexpr (OP != NsOp::kGram) t[r] = a.by_add * x[r] + t[r];
+        for (int r = 0; r < 8; ++r) t[r] = t[r] * (a.by_sum * kPerUnit);
+        if (OP != NsOp::kGram && live) {
+          const GLB char* p = (const GLB char*)add + m * a.pitch_d + part_at(n);
+          add_parts(*(const GLB u32x4*)p, *(const GLB u32x4*)(p + 64), a.by_add, t);
         }
         if (direct && live) {
           if (final_step)

@@ -52,14 +52,21 @@ __device__ __forceinline__ void load8(const void* x, int64_t i, int64_t left, fl
     for (int k = 0; k < 8; ++k) v[k] = k < left ? ld_elem<FMT>(x, i + k) : 0.0f;
   }
 }
+// v - h and by h + v, one instruction each that takes the fp16 value as it is (by a constant -1 it would be widened and
+// subtracted).
+__device__ __forceinline__ float less(float v, _Float16 h) {
+  float minus = -1.0f;
+  asm("" : "+s"(minus));
+  return __builtin_fmaf((float)h, minus, v);
+}
+__device__ __forceinline__ float plus(float v, float by, _Float16 h) { return __builtin_fmaf((float)h, by, v); }
 // Eight values as their parts.  (A product that the compiler folds into the conversion to hi is no matter: lo is what is
 // left of the fp32 value.)
 __device__ __forceinline__ void to_parts(const float* t, u32x4& hi, u32x4& lo) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const f16x2 h = __builtin_convertvector((f32x2){t[2 * k], t[2 * k + 1]}, f16x2);
-    const f32x2 back = __builtin_convertvector(h, f32x2);
-    const f16x2 l = __builtin_convertvector((f32x2){t[2 * k] - back[0], t[2 * k + 1] - back[1]}, f16x2);
+    const f16x2 l = __builtin_convertvector((f32x2){less(t[2 * k], h[0]), less(t[2 * k + 1], h[1])}, f16x2);
     hi[k] = __builtin_bit_cast(uint32_t, h);
     lo[k] = __builtin_bit_cast(uint32_t, l);
   }
@@ -73,13 +80,14 @@ __device__ __forceinline__ void store_parts(char* row, int64_t col, const float*
   *(GLB u32x4*)p = hi;
   *(GLB u32x4*)(p + 64) = lo;
 }
-__device__ __forceinline__ void load_parts(const char* row, int64_t col, float* t) {
-  const GLB char* p = (const GLB char*)row + part_at(col);
-  const u32x4 hi = *(const GLB u32x4*)p, lo = *(const GLB u32x4*)(p + 64);
+// t[k] += by times eight values held in parts, lo before hi.
+__device__ __forceinline__ void add_parts(u32x4 hi, u32x4 lo, float by, float* t) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    t[2 * k] = h_lo<kFP16>(hi[k]) + h_lo<kFP16>(lo[k]);
-    t[2 * k + 1] = h_hi<kFP16>(hi[k]) + h_hi<kFP16>(lo[k]);
+    const uint32_t two_hi = hi[k], two_lo = lo[k];  // (a bit cast of hi[k] itself takes hi[0])
+    const f16x2 h = __builtin_bit_cast(f16x2, two_hi), l = __builtin_bit_cast(f16x2, two_lo);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) t[2 * k + r] = plus(plus(t[2 * k + r], by, l[r]), by, h[r]);
   }
 }
 

@@ -45,10 +45,6 @@ __device__ __forceinline__ int small_at(int row, int piece) {
 template <int CA, int CB, bool TURNED, int FM>
 __device__ __forceinline__ void small_product(const LDS char* a, const LDS char* b, int groups, int wm, int wn, f32x4 (&acc)[FM][2]) {
   const int lane = threadIdx.x & 63, g = lane >> 4, i16 = lane & 15;
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = (f32x4){0, 0, 0, 0};
   // A lane's places: the xor of a place is of the lane alone, groups and fragments lie at fixed distances from it.
   const LDS char *at_a[2], *at_b[2], *at_t[2][2][2];
 #pragma unroll
@@ -61,7 +57,7 @@ __device__ __forceinline__ void small_product(const LDS char* a, const LDS char*
       for (int four = 0; four < 2; ++four)  // 8 rows (4 and 4) of the summed axis x 16 columns
         at_t[part][j][four] = b + small_at<CB>(8 * g + (i16 >> 2) + 4 * four, part * 4 + j * 2 + (i16 >> 1 & 1)) + (i16 & 1) * 8 + wn * 4;
   }
-  for (int k = 0; k < groups; ++k) {
+  auto group = [&](int k, auto first) {
     i32x4 fa[2][FM], fb[2][2];
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
@@ -83,13 +79,16 @@ __device__ __forceinline__ void small_product(const LDS char* a, const LDS char*
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mfma_f16(fb[p == 2][j], fa[p == 0][i], acc[i][j]);
-  }
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = mfma_f16(fb[p == 2][j], fa[p == 0][i], first && p == 0 ? (f32x4){0, 0, 0, 0} : acc[i][j]);
+  };
+  group(0, Yes{});
+  for (int k = 1; k < groups; ++k) group(k, No{});
 }
 
-// f(fragment, row, column of the first, 8 held values) for a wave's sums.
+// f(fragment, row, column of the first, 8 held values) for a wave's sums times `by`.
 template <int FM, class F>
-__device__ __forceinline__ void small_each(int wm, int wn, const f32x4 (&acc)[FM][2], F f) {
+__device__ __forceinline__ void small_each(int wm, int wn, const f32x4 (&acc)[FM][2], float by, F f) {
   const int lane = threadIdx.x & 63, g = lane >> 4, i16 = lane & 15;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -98,8 +97,8 @@ __device__ __forceinline__ void small_each(int wm, int wn, const f32x4 (&acc)[FM
     for (int r = 0; r < 4; ++r) {
       uint32_t lo, hi;
       trade(__float_as_uint(acc[i][0][r]), __float_as_uint(acc[i][1][r]), lo, hi);
-      t[r] = __uint_as_float(lo) * kPerUnit;
-      t[4 + r] = __uint_as_float(hi) * kPerUnit;
+      t[r] = __uint_as_float(lo) * by;
+      t[4 + r] = __uint_as_float(hi) * by;
     }
     f(i, wm + i * 16 + i16, wn + eight_at(g), t);
   }
@@ -114,13 +113,8 @@ __device__ __forceinline__ void small_put(LDS char* to, int row, int col, const 
 }
 template <int COLS>
 __device__ __forceinline__ void small_add(const LDS char* from, int row, int col, float by, float* t) {
-  const u32x4 hi = *(const LDS u32x4*)(from + small_at<COLS>(row, small_piece(col)));
-  const u32x4 lo = *(const LDS u32x4*)(from + small_at<COLS>(row, small_piece(col) + 4));
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    t[2 * k] = by * (h_lo<kFP16>(hi[k]) + h_lo<kFP16>(lo[k])) + t[2 * k];
-    t[2 * k + 1] = by * (h_hi<kFP16>(hi[k]) + h_hi<kFP16>(lo[k])) + t[2 * k + 1];
-  }
+  add_parts(*(const LDS u32x4*)(from + small_at<COLS>(row, small_piece(col))),
+            *(const LDS u32x4*)(from + small_at<COLS>(row, small_piece(col) + 4)), by, t);
 }
 // b S + c S^2 of the S in LDS (m x m, padded), in its place; barriers in it.
 template <int SIDE>
@@ -131,9 +125,9 @@ __device__ __forceinline__ void small_poly(LDS char* s, int m, int wm, int wn, f
   float b[L::FM][8];
   if (in_s) {
     small_product<SIDE, SIDE, false>(s, s, m / 32, wm, wn, acc);
-    small_each(wm, wn, acc, [&](int i, int row, int col, const float* t) {
+    small_each(wm, wn, acc, cc * kPerUnit, [&](int i, int row, int col, const float* t) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) b[i][k] = cc * t[k];
+      for (int k = 0; k < 8; ++k) b[i][k] = t[k];
       small_add<SIDE>(s, row, col, cb, b[i]);
     });
   }
@@ -244,14 +238,14 @@ __global__ __launch_bounds__(Small<SIDE>::kThreads) void ns_small(const SmallArg
     const float ca = a.coefs[3 * step], cb = a.coefs[3 * step + 1], cc = a.coefs[3 * step + 2];
     if (in_s) {
       small_product<SIDE, SIDE, false>(x, x, a.n / 32, wm, wn, acc);
-      small_each(wm, wn, acc, [&](int, int row, int col, const float* t) { small_put<SIDE>(s, row, col, t); });
+      small_each(wm, wn, acc, kPerUnit, [&](int, int row, int col, const float* t) { small_put<SIDE>(s, row, col, t); });
     }
     __syncthreads();
     small_poly<SIDE>(s, a.m, wm, wn, cb, cc);
     float b[L::FM][8];
     if (in_x) {
       small_product<SIDE, SIDE, true>(s, x, a.m / 32, wm, wn, acc);
-      small_each(wm, wn, acc, [&](int i, int row, int col, const float* t) {
+      small_each(wm, wn, acc, kPerUnit, [&](int i, int row, int col, const float* t) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) b[i][k] = t[k];
         small_add<SIDE>(x, row, col, ca, b[i]);
@@ -309,7 +303,7 @@ __global__ __launch_bounds__(Small<SIDE>::kThreads) void ns_slab(const NsSlab a)
   if (wm >= m || wn >= cols) return;
   f32x4 acc[FM][2];
   small_product<SIDE, kCols, true>(s, x, m / 32, wm, wn, acc);
-  small_each(wm, wn, acc, [&](int, int row, int col, const float* t) {
+  small_each(wm, wn, acc, kPerUnit, [&](int, int row, int col, const float* t) {
     float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = t[k];
