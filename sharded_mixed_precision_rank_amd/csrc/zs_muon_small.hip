@@ -4,9 +4,9 @@
 // three products of them, fp32 sums).
 //
 // Bound by a workgroup's LDS reads and the trips between them: 15 products of 128 x
-// 128 x 128, one behind the other, take 3.4 us each, whether one matrix or one for
-// every compute unit (32 of them, fp32 to bf16: 54 us, where a kernel for each
-// product took 96).  Reading fragments a group ahead was slower.
+// 128 x 128, one behind the other, take 2.9 us each, 1.3 of them matrix instructions,
+// whether one matrix or one for every compute unit (32 of them, fp32 to bf16: 46.6 us,
+// where a kernel for each product took 96).
 #include "zs_muon_dev.h"
 
 namespace zs {
@@ -29,11 +29,12 @@ struct SmallArgs {
 // A matrix of SIDE columns in LDS: rows of SIDE / 4 pieces of 16 bytes, in groups of 4 pieces of hi parts and 4 of lo
 // parts of 32 columns; piece c of row r lies at place c ^ (r & 7) of its group, so that 8 rows' equal pieces lie in
 // different banks.
-template <int SIDE>
+// A wave has ROWS rows of 32 columns.
+template <int SIDE, int ROWS>
 struct Small {
   static constexpr int kPitch = SIDE * 4, kBytes = SIDE * kPitch;
-  static constexpr int WM = 2, WN = SIDE / 32, kThreads = WM * WN * 64;
-  static constexpr int TM = SIDE / WM, FM = TM / 16;  // rows of a wave, which has 32 columns
+  static constexpr int WN = SIDE / 32, kThreads = SIDE / ROWS * WN * 64;
+  static constexpr int TM = ROWS, FM = TM / 16;
 };
 template <int COLS>
 __device__ __forceinline__ int small_at(int row, int piece) {
@@ -57,30 +58,43 @@ __device__ __forceinline__ void small_product(const LDS char* a, const LDS char*
       for (int four = 0; four < 2; ++four)  // 8 rows (4 and 4) of the summed axis x 16 columns
         at_t[part][j][four] = b + small_at<CB>(8 * g + (i16 >> 2) + 4 * four, part * 4 + j * 2 + (i16 >> 1 & 1)) + (i16 & 1) * 8 + wn * 4;
   }
-  auto group = [&](int k, auto first) {
-    i32x4 fa[2][FM], fb[2][2];
+  i32x4 fa[2][FM], fb[2][2];
+  auto read_a = [&](int part, int k) {
 #pragma unroll
-    for (int part = 0; part < 2; ++part) {
+    for (int i = 0; i < FM; ++i) fa[part][i] = *(const LDS i32x4*)(at_a[part] + i * 16 * CA * 4 + k * 128);
+  };
+  auto read_b = [&](int part, int k) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) fa[part][i] = *(const LDS i32x4*)(at_a[part] + i * 16 * CA * 4 + k * 128);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if constexpr (TURNED) {
-          const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(LDS char*)(at_t[part][j][0] + k * 32 * CB * 4));
-          const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(LDS char*)(at_t[part][j][1] + k * 32 * CB * 4));
-          fb[part][j] = __builtin_bit_cast(i32x4, (i16x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
-        } else {
-          fb[part][j] = *(const LDS i32x4*)(at_b[part] + j * 16 * CB * 4 + k * 128);
-        }
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (TURNED) {
+        const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(LDS char*)(at_t[part][j][0] + k * 32 * CB * 4));
+        const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS i16x4*)(LDS char*)(at_t[part][j][1] + k * 32 * CB * 4));
+        fb[part][j] = __builtin_bit_cast(i32x4, (i16x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]});
+      } else {
+        fb[part][j] = *(const LDS i32x4*)(at_b[part] + j * 16 * CB * 4 + k * 128);
       }
     }
+  };
+  auto times = [&](int pa, int pb, auto first) {
 #pragma unroll
-    for (int p = 0; p < 3; ++p)  // lo hi, hi hi, hi lo
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = mfma_f16(fb[p == 2][j], fa[p == 0][i], first && p == 0 ? (f32x4){0, 0, 0, 0} : acc[i][j]);
+      for (int j = 0; j < 2; ++j) acc[i][j] = mfma_f16(fb[pb][j], fa[pa][i], first ? (f32x4){0, 0, 0, 0} : acc[i][j]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // lo hi, hi hi, hi lo: the fragments of the next product, and of the next group's first, are read meanwhile (past the last
+  // group: again, which is never used)
+  read_a(1, 0);
+  read_b(0, 0);
+  auto group = [&](int k, auto first) {
+    const int next = k + 1 < groups ? k + 1 : k;
+    read_a(0, k);
+    read_b(1, k);
+    times(1, 0, first);
+    read_a(1, next);
+    times(0, 0, No{});
+    read_b(0, next);
+    times(0, 1, No{});
   };
   group(0, Yes{});
   for (int k = 1; k < groups; ++k) group(k, No{});
@@ -117,9 +131,9 @@ __device__ __forceinline__ void small_add(const LDS char* from, int row, int col
             *(const LDS u32x4*)(from + small_at<COLS>(row, small_piece(col) + 4)), by, t);
 }
 // b S + c S^2 of the S in LDS (m x m, padded), in its place; barriers in it.
-template <int SIDE>
+template <int SIDE, int ROWS>
 __device__ __forceinline__ void small_poly(LDS char* s, int m, int wm, int wn, float cb, float cc) {
-  typedef Small<SIDE> L;
+  typedef Small<SIDE, ROWS> L;
   const bool in_s = wm < m && wn < m;
   f32x4 acc[L::FM][2];
   float b[L::FM][8];
@@ -149,9 +163,9 @@ __device__ __forceinline__ void small_last(const NsLast& a, int64_t batch, int64
   }
 }
 
-template <int SIDE, int FMT, bool UPDATE>
-__global__ __launch_bounds__(Small<SIDE>::kThreads) void ns_small(const SmallArgs a) {
-  typedef Small<SIDE> L;
+template <int SIDE, int ROWS, int FMT, bool UPDATE>
+__global__ __launch_bounds__((Small<SIDE, ROWS>::kThreads)) void ns_small(const SmallArgs a) {
+  typedef Small<SIDE, ROWS> L;
   constexpr int kPieces = SIDE * SIDE / 8 / L::kThreads;  // of 8 values a thread
   __shared__ __attribute__((aligned(1024))) char lds[2 * L::kBytes];
   __shared__ double sums[L::kThreads / 64];
@@ -241,7 +255,7 @@ __global__ __launch_bounds__(Small<SIDE>::kThreads) void ns_small(const SmallArg
       small_each(wm, wn, acc, kPerUnit, [&](int, int row, int col, const float* t) { small_put<SIDE>(s, row, col, t); });
     }
     __syncthreads();
-    small_poly<SIDE>(s, a.m, wm, wn, cb, cc);
+    small_poly<SIDE, ROWS>(s, a.m, wm, wn, cb, cc);
     float b[L::FM][8];
     if (in_x) {
       small_product<SIDE, SIDE, true>(s, x, a.m / 32, wm, wn, acc);
@@ -254,8 +268,10 @@ __global__ __launch_bounds__(Small<SIDE>::kThreads) void ns_small(const SmallArg
     const int lane = tid & 63, col = wn + eight_at(lane >> 4);
     if (step == a.steps - 1) {
       if (!in_x) return;
+      int row_last = wm + (lane & 15), col_last = col;
+      asm volatile("" : "+v"(row_last), "+v"(col_last));  // (so that the places in memory are not held through all steps)
 #pragma unroll
-      for (int i = 0; i < L::FM; ++i) small_last(a.last, batch, wm + i * 16 + (lane & 15), col, b[i]);
+      for (int i = 0; i < L::FM; ++i) small_last(a.last, batch, row_last + i * 16, col_last, b[i]);
       return;
     }
     __syncthreads();  // X has been read
@@ -275,8 +291,8 @@ __global__ __launch_bounds__(Small<SIDE>::kThreads) void ns_small(const SmallArg
 // the two, and longer where there are more workgroups than compute units.)
 // ---------------------------------------------------------------------------
 template <int SIDE>
-__global__ __launch_bounds__(Small<SIDE>::kThreads) void ns_slab(const NsSlab a) {
-  typedef Small<SIDE> L;
+__global__ __launch_bounds__((Small<SIDE, 32>::kThreads)) void ns_slab(const NsSlab a) {
+  typedef Small<SIDE, 32> L;
   constexpr int kCols = 64, FM = 2;
   static_assert(L::kThreads / 64 == SIDE / 32 * 2, "32 x 32 values a wave");
   __shared__ __attribute__((aligned(1024))) char lds[L::kBytes + SIDE * kCols * 4];
@@ -298,7 +314,7 @@ __global__ __launch_bounds__(Small<SIDE>::kThreads) void ns_slab(const NsSlab a)
       *(LDS u32x4*)(x + small_at<kCols>(row, piece)) = *(const GLB u32x4*)(const GLB char*)(from_x + (int64_t)row * a.pitch_x + piece * 16);
   }
   __syncthreads();
-  small_poly<SIDE>(s, m, wave / L::WN * L::TM, wave % L::WN * 32, a.cb, a.cc);
+  small_poly<SIDE, 32>(s, m, wave / L::WN * L::TM, wave % L::WN * 32, a.cb, a.cc);
   const int wm = wave / 2 * 32, wn = wave % 2 * 32;
   if (wm >= m || wn >= cols) return;
   f32x4 acc[FM][2];
@@ -315,7 +331,7 @@ __global__ __launch_bounds__(Small<SIDE>::kThreads) void ns_slab(const NsSlab a)
   });
 }
 
-template <int SIDE>
+template <int SIDE, int ROWS>
 hipError_t small_launch(const NsProblem& p, hipStream_t stream) {
   SmallArgs a{};
   a.m = (int32_t)padded(p.rows < p.cols ? p.rows : p.cols);
@@ -326,18 +342,18 @@ hipError_t small_launch(const NsProblem& p, hipStream_t stream) {
   const dim3 grid((unsigned)p.batch);
   if (p.update) {
     a.mean = mean_of(p);
-    ns_small<SIDE, kFP32, true><<<grid, Small<SIDE>::kThreads, 0, stream>>>(a);
+    ns_small<SIDE, ROWS, kFP32, true><<<grid, Small<SIDE, ROWS>::kThreads, 0, stream>>>(a);
     return hipGetLastError();
   }
   a.x = p.x;
   a.ld = p.ld_x;
   a.batch_ld = p.batch_x;
   if (p.x_format == ZS_FORMAT_FP32)
-    ns_small<SIDE, kFP32, false><<<grid, Small<SIDE>::kThreads, 0, stream>>>(a);
+    ns_small<SIDE, ROWS, kFP32, false><<<grid, Small<SIDE, ROWS>::kThreads, 0, stream>>>(a);
   else if (p.x_format == ZS_FORMAT_BF16)
-    ns_small<SIDE, kBF16, false><<<grid, Small<SIDE>::kThreads, 0, stream>>>(a);
+    ns_small<SIDE, ROWS, kBF16, false><<<grid, Small<SIDE, ROWS>::kThreads, 0, stream>>>(a);
   else
-    ns_small<SIDE, kFP16, false><<<grid, Small<SIDE>::kThreads, 0, stream>>>(a);
+    ns_small<SIDE, ROWS, kFP16, false><<<grid, Small<SIDE, ROWS>::kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -347,14 +363,17 @@ namespace ns {
 
 hipError_t launch_ns_slab(const NsSlab& a, int64_t batch, hipStream_t stream) {
   const dim3 grid((unsigned)((a.n + 63) / 64), (unsigned)batch);
-  ns_slab<kSlabSide><<<grid, Small<kSlabSide>::kThreads, 0, stream>>>(a);
+  ns_slab<kSlabSide><<<grid, Small<kSlabSide, 32>::kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace ns
 
 hipError_t launch_ns_small(const NsProblem& p, hipStream_t stream) {
-  return p.rows <= 64 && p.cols <= 64 ? small_launch<64>(p, stream) : small_launch<kSmallSide>(p, stream);
+  if (p.rows <= 64 && p.cols <= 64) return small_launch<64, 32>(p, stream);
+  // 16 waves of 32 rows where some of them have nothing but padding (32 x 96 x 128: 35.1 us, 8 waves of 64 rows 40.5), 8 where
+  // all have work (32 x 128 x 128: 46.6, 16 waves 51.8)
+  return p.rows <= 96 || p.cols <= 96 ? small_launch<kSmallSide, 32>(p, stream) : small_launch<kSmallSide, 64>(p, stream);
 }
 
 }  // namespace zs

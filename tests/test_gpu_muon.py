@@ -284,6 +284,15 @@ def test_reduce_muon_at_odd_addresses(zs):
     assert all(torch.equal(a, b) for a, b in zip(*results))
 
 
+@pytest.mark.parametrize("rows,cols", [(96, 128), (128, 96), (97, 128), (128, 97), (128, 128), (65, 33), (33, 65), (128, 1)])
+def test_matrices_of_one_workgroup(zs, rows, cols):
+    """Both sides at most 128, by either count of waves: products to their one rounding, default steps, the update."""
+    for coefs in ((1.0, 1.0, 0.0), (1.0, 0.0, 1.0)):
+        test_exact_products(zs, rows, cols, coefs)
+    test_default_steps(zs, rows, cols, "bf16", "fp32")
+    test_reduce_muon(zs, (3, rows, cols), 2, True)
+
+
 @pytest.mark.parametrize("shape", [(96, 200), (2, 64, 64), (700, 520)])
 def test_graph_replays_and_streams(zs, shape):
     """Captured with its own workspace, replayed between eager steps on another: both walk the same path of states."""
