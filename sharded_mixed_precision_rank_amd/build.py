@@ -18,7 +18,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("zs_kernels.hip", "zs_twopass.hip", "
 HOST_SOURCES = [os.path.join(CSRC, "zs_cpu_adam.cpp")]
 HOST_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-ffp-contract=off", "-fno-fast-math", "-Wall"]
 FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
     # one rounding per operation, correctly rounded divide and sqrt
     "-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt",
     # no packed fp32 instructions
@@ -27,8 +27,7 @@ FLAGS = [
 ]
 
 
-def _hipcc(args, verbose):
-    cmd = ["hipcc", *FLAGS, *args]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -38,6 +37,15 @@ def _hipcc(args, verbose):
         raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs))
+
+
+def _hipcc(sources, objs, out, extra, verbose):
+    cmd = ["hipcc", *FLAGS, *extra]
+    for src in sources:
+        cmd += ["-x", "hip", src]
+    if objs:
+        cmd += ["-x", "none", *objs]
+    _run(cmd + ["-o", out], verbose)
 
 
 def build(verbose: bool = False, out: str = LIB, extra=()) -> str:
@@ -53,12 +61,12 @@ def build(verbose: bool = False, out: str = LIB, extra=()) -> str:
     with tempfile.TemporaryDirectory() as tmp:
         def compile_one(src):
             obj = os.path.join(tmp, os.path.basename(src) + ".o")
-            _hipcc([*extra, "-c", "-x", "hip", src, "-o", obj], verbose)
+            _run(["hipcc", *(f for f in FLAGS if f != "-shared"), *extra, "-c", "-x", "hip", src, "-o", obj], verbose)
             return obj
 
         with concurrent.futures.ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
             device = list(pool.map(compile_one, SOURCES))
-        _hipcc([*device, *objs, "-shared", "-o", out], verbose)
+        _hipcc([], [*device, *objs], out, [], verbose)
     return out
 
 
