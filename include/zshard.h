@@ -663,8 +663,9 @@ ZS_API zs_status zs_orthogonalize(const void* x, int32_t x_format, int64_t ld_x,
    grad_chunks: N bf16 arrays, 1 <= N <= ZS_MAX_REPLICAS (the host array is read
    during the call).  Any alignment of the elements.  master, momentum and
    param_bf16 are updated; no array may overlap another one.
-   Errors as zs_orthogonalize (hyperparameters not finite, lr, momentum or
-   weight_decay below 0, momentum 1 or more: ZS_ERR_RANGE). */
+   Errors as zs_orthogonalize (hyperparameters not finite, lr * scale or lr *
+   weight_decay past fp32's range, lr, momentum or weight_decay below 0, momentum 1
+   or more: ZS_ERR_RANGE). */
 ZS_API zs_status zs_reduce_muon(const uint16_t* const* grad_chunks, int32_t N, int64_t batch, int64_t rows, int64_t cols,
                                 float* master, float* momentum, uint16_t* param_bf16, const zs_muon_hp* hp,
                                 void* workspace, size_t workspace_bytes, zs_stream stream);

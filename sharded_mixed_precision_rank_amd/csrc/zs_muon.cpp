@@ -124,6 +124,13 @@ zs_status zs_reduce_muon(const uint16_t* const* grad_chunks, int32_t N, int64_t 
     return api_fail(ZS_ERR_RANGE, "lr and weight_decay must be >= 0 (got %g, %g)", hp->lr, hp->weight_decay);
   if (!(hp->momentum >= 0 && hp->momentum < 1)) return api_fail(ZS_ERR_RANGE, "momentum must be in [0, 1) (got %g)", hp->momentum);
   if (hp->nesterov != 0 && hp->nesterov != 1) return api_fail(ZS_ERR_RANGE, "nesterov must be 0 or 1 (got %d)", hp->nesterov);
+  p.mu = (float)hp->momentum;
+  p.dk = (float)(1.0 - hp->lr * hp->weight_decay);
+  p.ss = (float)(hp->lr * hp->scale);
+  // (an infinite factor would make NaN of an update of zeros)
+  if (!std::isfinite(p.dk) || !std::isfinite(p.ss))
+    return api_fail(ZS_ERR_RANGE, "lr * weight_decay and lr * scale must be fp32 values (got %g and %g)", hp->lr * hp->weight_decay,
+                    hp->lr * hp->scale);
   if (batch == 0 || rows == 0 || cols == 0) return ZS_OK;
   const int64_t n = batch * rows * cols;
   if ((double)batch * (double)rows * (double)cols * 4.0 > kMaxBytes)
@@ -155,9 +162,6 @@ zs_status zs_reduce_muon(const uint16_t* const* grad_chunks, int32_t N, int64_t 
   p.grads = grad_chunks;
   p.n_rep = N;
   p.nesterov = hp->nesterov;
-  p.mu = (float)hp->momentum;
-  p.dk = (float)(1.0 - hp->lr * hp->weight_decay);
-  p.ss = (float)(hp->lr * hp->scale);
   p.momentum = momentum;
   p.master = master;
   p.param = param_bf16;

@@ -112,3 +112,10 @@ def test_binding_refuses():
         zs.orthogonalize(x, x.clone(), coefs=(1, 2))
     with pytest.raises(ValueError, match="device tensor"):
         zs.reduce_muon([x.bfloat16()], x, x.clone(), x.bfloat16(), zs.MuonHP())
+
+
+@pytest.mark.parametrize("hp", [dict(lr=1e30, scale=1e30), dict(lr=1e30, scale=-1e30), dict(lr=1e30, weight_decay=1e30),
+                                dict(lr=1e200, weight_decay=1e200, scale=0.0), dict(lr=1e200, scale=1e200)])
+def test_reduce_muon_refuses_what_leaves_fp32_when_folded(hp):
+    """lr * scale and 1 - lr * weight_decay are fp32 values of the step: past that range, inf * 0 would be NaN in the master."""
+    assert zs.STATUS[muon(**hp)] == R and b"fp32" in LIB.zs_last_error(), LIB.zs_last_error()
