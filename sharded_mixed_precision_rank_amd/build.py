@@ -66,7 +66,7 @@ def build(verbose: bool = False, out: str = LIB, extra=()) -> str:
 
         with concurrent.futures.ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
             device = list(pool.map(compile_one, SOURCES))
-        _hipcc([], [*device, *objs], out, [], verbose)
+        _hipcc([], [*device, *objs], out, extra, verbose)
     return out
 
 

@@ -29,3 +29,13 @@ def test_the_librarys_compiler_call_takes_sources_and_objects(tmp_path):
     (tmp_path / "a.hip").write_text('extern "C" __attribute__((visibility("default"))) int a() { return 1; }\n')
     lib._hipcc([str(tmp_path / "a.hip")], [], str(tmp_path / "a.so"), [], False)
     assert ctypes.CDLL(str(tmp_path / "a.so")).a() == 1
+
+
+def test_extra_flags_reach_every_compile_and_the_link(monkeypatch, tmp_path):
+    lib = script("sharded_mixed_precision_rank_amd/build.py")
+    calls = []
+    monkeypatch.setattr(lib, "_run", lambda cmd, verbose: calls.append(cmd))
+    monkeypatch.setattr(lib.subprocess, "run", lambda *args, **kw: None)
+    lib.build(out=str(tmp_path / "built.so"), extra=("-lextra",))
+    assert len(calls) == len(lib.SOURCES) + 1 and calls[-1][-1] == str(tmp_path / "built.so")
+    assert all("-lextra" in cmd for cmd in calls)
