@@ -554,7 +554,7 @@ ZS_API zs_status zs_q8_weight_grad(const void* dy, int32_t dy_format, int64_t ld
  * range becomes an infinity.
  * ------------------------------------------------------------------------- */
 
-/* Activations (v: a value of gate). */
+/* Activations (v: a value of gate).  Their tails go down to fp32's subnormals. */
 #define ZS_ACT_SILU 0      /* v / (1 + e^-v) */
 #define ZS_ACT_GELU 1      /* v (1 + erf(v / sqrt 2)) / 2 */
 #define ZS_ACT_GELU_TANH 2 /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */

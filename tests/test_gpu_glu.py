@@ -384,3 +384,37 @@ def test_real_sizes(zs, T, N, K, kind):
     for got, want, roundings in checks:
         off = ((got.double() - want).norm() / want.norm()).item()
         assert off <= roundings * ref.half_step(kind) + 1e-5, off
+
+
+# every bf16 value in a range where the activation falls from 2^-110 to below bf16's smallest
+TAILS = {"silu": (-110.0, -76.0), "gelu": (-14.5, -12.0), "gelu_tanh": (-11.0, -9.0)}
+
+
+@pytest.mark.parametrize("act", TAILS)
+def test_tails_of_the_activations(zs, act):
+    """Where act and its slope are far below 2^-100 they are still bf16 values, normal ones down to 2^-126."""
+    lo, hi = (torch.tensor(v, dtype=torch.bfloat16).view(torch.int16).item() for v in TAILS[act])
+    gate = torch.arange(hi, lo + 1, dtype=torch.int16).view(torch.bfloat16)  # (of negative values the larger bits are lower)
+    n = gate.numel()
+    rng = np.random.default_rng(n)
+    up, dh = (torch.from_numpy(rng.uniform(0.3, 3.0, n) * rng.choice((-1, 1), n)).bfloat16() for _ in range(2))
+    value, slope = ref.act(gate.double(), act)
+    if act == "gelu_tanh":  # (1 - tanh^2 by the logistic function: 4 s(z) s(-z))
+        c, v = 2 * math.sqrt(2 / math.pi), gate.double()
+        z = c * (v + 0.044715 * v ** 3)
+        slope = torch.sigmoid(z) * (1 + v * torch.sigmoid(-z) * c * (1 + 3 * 0.044715 * v * v))
+    assert value.abs().max() > 2.0 ** -112 and 0 < value.abs().min() < 2.0 ** -133
+    assert ((value.abs() < 2.0 ** -120) & (value.abs() > 2.0 ** -126)).sum() >= 2
+    # fp32 steps: an exponent's argument of at most 160, off by 3 roundings of 2^-24 and 2^-18: below 2^-14 relative; where a
+    # factor is subnormal by 2^-147 (a rounding of 2^-150 and its like for the error function), times gate in a product
+    off_value = 2.0 ** -14 * value.abs() + 2.0 ** -147 * gate.double().abs()
+    off_slope = 2.0 ** -14 * slope.abs() + 2.0 ** -147 * gate.double().abs() ** 2
+    new = lambda: torch.empty(1, n, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    h, dg, du, again = new(), new(), new(), new()
+    x = torch.ones(1, 1, dtype=torch.bfloat16, device="cuda")
+    zs.glu_forward(x, gate[:, None].cuda(), up[:, None].cuda(), h, act=act)
+    zs.glu_backward(dh[None].cuda(), gate[None].cuda(), up[None].cuda(), dg, du, h=again, act=act)
+    near(h[0], value * up.double(), "bf16", off_value * up.double().abs())
+    near(again[0], value * up.double(), "bf16", off_value * up.double().abs())
+    near(du[0], value * dh.double(), "bf16", off_value * dh.double().abs())
+    near(dg[0], slope * up.double() * dh.double(), "bf16", off_slope * (up.double() * dh.double()).abs() + 2.0 ** -148)
