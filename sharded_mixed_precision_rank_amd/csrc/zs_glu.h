@@ -3,16 +3,12 @@
 // (elementwise gradients).  Not installed; not part of the ABI.
 #pragma once
 
+#include "zs_glu_choice.h"
 #include "zs_internal.h"
 
 namespace zs {
 
-// Leading dimensions are in elements of their own array.  The three products,
-// M x N outputs over a summed axis of K:
-//   kForward  a = x [M][K], b = w_gate and w_up [N][K]; out[0] = h, out[1], out[2] = gate, up (NULL: not kept)
-//   kInput    a = dgate and dup [M][K], b = w_gate and w_up [K][N]; out[0] = dx, both products in one sum
-//   kWeight   a = dgate and dup [K][M], b = x [K][N]; out[0], out[1] = dw_gate, dw_up (+ add[0], add[1])
-enum class GluOp : int32_t { kForward = 0, kInput = 1, kWeight = 2 };
+// Leading dimensions are in elements of their own array.
 struct GluGemm {
   const void* a[2];
   int64_t lda;

@@ -5,8 +5,6 @@
 //   kWeight   dWg = dgate^T x, dWu = dup^T x      (+ earlier micro-batches' sums), two products in one launch
 //
 // Operands are bf16 or fp16, sums fp32, each output rounded once.
-#include <cmath>
-
 #include "zs_act.h"
 #include "zs_glu.h"
 #include "zs_tile_dev.h"
@@ -15,6 +13,7 @@ namespace zs {
 namespace {
 
 using namespace dev;
+using namespace glu;
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -127,7 +126,6 @@ __device__ __forceinline__ i32x4 inside(int left) {
 // one barrier a stage.  Forward: 32 columns of gate beside the same 32 of up.
 // ---------------------------------------------------------------------------
 constexpr int kAnyTile = 64;
-constexpr int kStage = 64;  // of the summed axis a stage: 128 bytes of a row
 
 template <GluOp OP, int FMT>
 __global__ __launch_bounds__(256) void glu_any(const GluGemm a, int64_t tiles_n, int64_t tiles) {
@@ -787,73 +785,25 @@ hipError_t input_split_launch(const GluGemm& a, hipStream_t stream) {
 bool rows4(const void* p, int64_t rows, int64_t ld) {
   return (uintptr_t)p % 4 == 0 && (rows <= 1 || (ld % 2 == 0 && ld <= (1 << 21)));
 }
-int64_t tiles_of(const GluGemm& a, int64_t bm, int64_t bn) { return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn); }
-constexpr int64_t kMostTiles = 1 << 22;
-
-// The kernel of a product with rows on 4-byte boundaries, by the time it takes: a start, and so much a stage of 64 of the summed axis,
-// between `few` for a few workgroups and `full` for as many as run at once; more go in rounds (half overlapped) with a
-// start of their own.  us, fitted to 54 shapes from 1 to 9683 tokens on 256 compute units, inputs from memory: off by 6 to
-// 20%, and what it picks is 1.0 to 1.8% behind the best kernel's time in the mean.  For example, forward: 1 x 1024 x 1024 4.9 by
-// kFew, 6.4 by k64x32, 7.8 by k64; 61 x 4096 x 4096 55 / 18.1 / 20.7, 27.2 by k128; 333 x 11008 x 4096 136 by k64, 96 by k128, 88 by k192,
-// 100 by k256; input gradient: 61 x 4096 x 4096 23.9 by kSplit, 37 by k32, 67 by k128; 1025 x 1376 x 4096 118 by kSplit, 56 by k128, 43 by
-// k128Near, 60 by k256; weight gradients: 61 x 4096 x 4096 25.7 by k64, 22.9 by k128Near, 20.4 by k256.
-enum class GluTile { kFew, kSplit, k64x32, k32, k64, k64x128, k128, k128Near, k192, k256 };
-struct TileCost {
-  GluTile tile;
-  int bm, bn, at_once;  // sums of a workgroup; workgroups at once
-  double start, few, full, round;
-};
-constexpr TileCost kForwardCosts[] = {{GluTile::kFew, 16, 32, 2048, 3.68, 0.089, 1.459, 0.0},
-                                      {GluTile::k64x32, 64, 32, 256, 3.74, 0.200, 0.237, 1.24},
-                                      {GluTile::k64, 64, 64, 512, 3.80, 0.243, 0.455, 0.40},
-                                      {GluTile::k128, 128, 128, 256, 4.50, 0.324, 0.516, 2.14},
-                                      {GluTile::k192, 192, 128, 512, 6.00, 0.564, 1.195, 2.32},
-                                      {GluTile::k256, 256, 256, 256, 7.00, 0.972, 1.518, 3.42}};
-constexpr TileCost kInputCosts[] = {{GluTile::kSplit, 16, 64, 256, 3.02, 0.124, 0.165, 1.30},
-                                    {GluTile::k32, 32, 64, 512, 3.40, 0.248, 0.334, 0.72},
-                                    {GluTile::k64x128, 64, 128, 256, 4.54, 0.356, 0.435, 1.48},
-                                    {GluTile::k128, 128, 128, 256, 5.00, 0.452, 0.603, 2.11},
-                                    {GluTile::k128Near, 128, 128, 512, 5.00, 0.647, 1.008, 2.00},
-                                    {GluTile::k256, 256, 256, 256, 7.00, 1.092, 1.548, 0.99}};
-constexpr TileCost kWeightCosts[] = {{GluTile::k64, 64, 64, 1024, 3.99, 0.294, 0.745, 2.01},
-                                     {GluTile::k128, 128, 128, 256, 5.14, 0.406, 0.527, 2.55},
-                                     {GluTile::k128Near, 128, 128, 512, 6.59, 0.460, 0.899, 3.05},
-                                     {GluTile::k256, 256, 256, 256, 8.99, 1.156, 1.454, 5.34}};
-template <size_t N>
-GluTile cheapest(const TileCost (&costs)[N], const GluGemm& a, int64_t wide, int64_t parts, int64_t stages) {
-  double least = 1e300;
-  GluTile best = costs[N - 1].tile;
-  for (const TileCost& c : costs) {
-    const double x = (double)(parts * ((a.M + c.bm - 1) / c.bm) * ((wide + c.bn - 1) / c.bn)) / c.at_once;
-    const double stage = c.few + (c.full - c.few) * (x < 1 ? x : 1);
-    const double us = x <= 1 ? c.start + stage * (double)stages : c.start + 0.5 * (x + std::ceil(x)) * (c.round + stage * (double)stages);
-    if (us < least) least = us, best = c.tile;
-  }
-  return best;
-}
 
 template <GluOp OP, int FMT>
 hipError_t gemm_launch(const GluGemm& given, hipStream_t stream) {
   GluGemm a = given;
   const bool weight = OP == GluOp::kWeight, forward = OP == GluOp::kForward;
   const int64_t rows_a = weight ? a.K : a.M, rows_b = forward ? a.N : a.K;
-  bool fast = a.K > 0 && tiles_of(a, 64, 32) < kMostTiles && rows4(a.a[0], rows_a, a.lda) && rows4(a.b[0], rows_b, a.ldb);
-  if (!forward) fast = fast && rows4(a.a[1], rows_a, a.lda);
-  if (!weight) fast = fast && rows4(a.b[1], rows_b, a.ldb);
-  if (!weight) fast = fast && a.K <= (1 << 21);  // (a single row may be longer)
-  const int64_t parts = weight ? 2 : 1;
-  if (!fast) {
-    const int64_t tiles = parts * tiles_of(a, 128, forward ? 64 : 128);
-    if (a.K == 0 || tiles < 64 || tiles >= kMostTiles) return any_launch<OP, FMT>(a, stream);
-    return tile_launch<OP, FMT, 128, 128, 2, 2, 2, true>(a, stream);
-  }
+  bool direct = rows4(a.a[0], rows_a, a.lda) && rows4(a.b[0], rows_b, a.ldb);
+  if (!forward) direct = direct && rows4(a.a[1], rows_a, a.lda);
+  if (!weight) direct = direct && rows4(a.b[1], rows_b, a.ldb);
+  if (!weight) direct = direct && a.K <= (1 << 21);  // (a single row may be longer)
+  const GluTile tile = choose(OP, a.M, a.N, a.K, direct);
+  if (tile == GluTile::kAny) return any_launch<OP, FMT>(a, stream);
+  if (tile == GluTile::kThrough) return tile_launch<OP, FMT, 128, 128, 2, 2, 2, true>(a, stream);
   // a single row: any distance that holds what a tile reads of it
   const int64_t wide_a = weight ? 256 : a.K, wide_b = forward ? a.K : 256;
   if (rows_a <= 1) a.lda = (wide_a + 255) / 256 * 256;
   if (rows_b <= 1) a.ldb = (wide_b + 255) / 256 * 256;
-  const int64_t stages = (a.K + kStage - 1) / kStage;
   if constexpr (OP == GluOp::kForward) {
-    switch (cheapest(kForwardCosts, a, 2 * a.N, 1, stages)) {
+    switch (tile) {
       case GluTile::kFew: return few_launch<FMT>(a, stream);
       case GluTile::k64x32: return tile_launch<OP, FMT, 64, 32, 4, 1, 8>(a, stream);
       case GluTile::k64: return tile_launch<OP, FMT, 64, 64, 4, 1, 4>(a, stream);
@@ -862,7 +812,7 @@ hipError_t gemm_launch(const GluGemm& given, hipStream_t stream) {
       default: return tile_launch<OP, FMT, 256, 256, 2, 4, 2>(a, stream);
     }
   } else if constexpr (OP == GluOp::kInput) {
-    switch (cheapest(kInputCosts, a, a.N, 1, 2 * stages)) {
+    switch (tile) {
       case GluTile::kSplit: return input_split_launch<FMT>(a, stream);
       case GluTile::k32: return tile_launch<OP, FMT, 32, 64, 2, 2, 4>(a, stream);
       case GluTile::k64x128: return tile_launch<OP, FMT, 64, 128, 2, 2, 4>(a, stream);
@@ -871,7 +821,7 @@ hipError_t gemm_launch(const GluGemm& given, hipStream_t stream) {
       default: return tile_launch<OP, FMT, 256, 256, 2, 4, 2>(a, stream);
     }
   } else {
-    switch (cheapest(kWeightCosts, a, a.N, 2, stages)) {
+    switch (tile) {
       case GluTile::k64: return tile_launch<OP, FMT, 64, 64, 4, 1, 2>(a, stream);
       case GluTile::k128: return tile_launch<OP, FMT, 128, 128, 4, 2, 4>(a, stream);
       case GluTile::k128Near: return tile_launch<OP, FMT, 128, 128, 2, 2, 2>(a, stream);

@@ -6,6 +6,7 @@
 #include <stddef.h>
 
 #include "zs_internal.h"
+#include "zs_muon_choice.h"
 
 namespace zs {
 
@@ -41,8 +42,7 @@ struct NsProblem {
 size_t ns_workspace_bytes(int64_t rows, int64_t cols, int64_t batch);
 hipError_t launch_ns(const NsProblem& p, void* workspace, hipStream_t stream);
 
-// Matrices that a workgroup does by itself, from values to values (zs_muon_small.hip).
-constexpr int64_t kSmallSide = 128;
+// Matrices with sides of at most ns::kSmallSide, from values to values (zs_muon_small.hip).
 hipError_t launch_ns_small(const NsProblem& p, hipStream_t stream);
 
 }  // namespace zs

@@ -17,8 +17,6 @@ constexpr float kUnit = 4096.0f;           // held values are this times the mat
 constexpr float kPerUnit = 1.0f / 4096.0f;
 constexpr int kMostPartials = 1024;        // sums of squares of a matrix
 
-inline int64_t padded(int64_t n) { return (n + 31) / 32 * 32; }
-
 struct MeanArgs {
   const uint16_t* g[ZS_MAX_REPLICAS];
   float* momentum;
@@ -201,7 +199,6 @@ inline MeanArgs mean_of(const NsProblem& p) {
 }
 
 // The rest of a step of a matrix with at most kSlabSide rows, from its S (zs_muon_small.hip).
-constexpr int64_t kSlabSide = 64;
 struct NsSlab {
   const char *s, *x;
   char* to;  // NULL: the last step
