@@ -18,7 +18,7 @@ enum class GluOp : int32_t { kForward = 0, kInput = 1, kWeight = 2 };
 namespace glu {
 
 constexpr int kStage = 64;  // of the summed axis a stage: 128 bytes of a row
-constexpr int64_t kMostTiles = 1 << 22;
+constexpr int64_t kMostTiles = 1 << 22;  // workgroups along a grid's first axis: 2^31 threads at most
 
 // The kernel of a product with rows on 4-byte boundaries, by the time it takes: a start, and so much a stage of 64 of the summed axis,
 // between `few` for a few workgroups and `full` for as many as run at once; more go in rounds (half overlapped) with a
@@ -49,25 +49,28 @@ constexpr TileCost kWeightCosts[] = {{GluTile::k64, 64, 64, 1024, 3.99, 0.294, 0
                                      {GluTile::k128, 128, 128, 256, 5.14, 0.406, 0.527, 2.55},
                                      {GluTile::k128Near, 128, 128, 512, 6.59, 0.460, 0.899, 3.05},
                                      {GluTile::k256, 256, 256, 256, 8.99, 1.156, 1.454, 5.34}};
+inline int64_t tiles_of(int64_t M, int64_t N, int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); }
+// kAny: too many tiles of every kind.
 template <size_t COSTS>
 GluTile cheapest(const TileCost (&costs)[COSTS], int64_t M, int64_t wide, int64_t parts, int64_t stages) {
   double least = 1e300;
-  GluTile best = costs[COSTS - 1].tile;
+  GluTile best = GluTile::kAny;
   for (const TileCost& c : costs) {
-    const double x = (double)(parts * ((M + c.bm - 1) / c.bm) * ((wide + c.bn - 1) / c.bn)) / c.at_once;
+    const int64_t tiles = tiles_of(M, wide, c.bm, c.bn);
+    if (tiles >= kMostTiles) continue;
+    const double x = (double)(parts * tiles) / c.at_once;
     const double stage = c.few + (c.full - c.few) * (x < 1 ? x : 1);
     const double us = x <= 1 ? c.start + stage * (double)stages : c.start + 0.5 * (x + std::ceil(x)) * (c.round + stage * (double)stages);
     if (us < least) least = us, best = c.tile;
   }
   return best;
 }
-inline int64_t tiles_of(int64_t M, int64_t N, int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); }
 
 // `direct`: rows that the direct loads to LDS take.
 inline GluTile choose(GluOp op, int64_t M, int64_t N, int64_t K, bool direct) {
   const int64_t stages = (K + kStage - 1) / kStage, parts = op == GluOp::kWeight ? 2 : 1;
   if (K == 0) return GluTile::kAny;
-  if (!direct || tiles_of(M, N, 64, 32) >= kMostTiles) {
+  if (!direct) {
     const int64_t tiles = parts * tiles_of(M, N, 128, op == GluOp::kForward ? 64 : 128);
     return tiles < 64 || tiles >= kMostTiles ? GluTile::kAny : GluTile::kThrough;
   }

@@ -418,3 +418,27 @@ def test_tails_of_the_activations(zs, act):
     near(again[0], value * up.double(), "bf16", off_value * up.double().abs())
     near(du[0], value * dh.double(), "bf16", off_value * dh.double().abs())
     near(dg[0], slope * up.double() * dh.double(), "bf16", off_slope * (up.double() * dh.double()).abs() + 2.0 ** -148)
+
+
+def test_outputs_past_the_small_tiles_count(zs):
+    """More outputs than 2^22 tiles of 64 x 32: the last rows are right and the others zeros, forward and back."""
+    T, N, K = 800_000, 11008, 64
+    new = lambda r, c: torch.zeros(r, c, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    rng = np.random.default_rng(2)
+    last = slice(T - 3, T)
+    for first in (True, False):
+        out = torch.full((T, N), 5.0, dtype=torch.bfloat16, device="cuda")
+        if first:
+            x, wg, wu = new(T, K), whole(rng, N, K).bfloat16().cuda(), whole(rng, N, K).bfloat16().cuda()
+            x[last] = whole(rng, 3, K).bfloat16().cuda()
+            zs.glu_forward(x, wg, wu, out, act="relu")
+            want = ref.forward(x[last].cpu(), wg.cpu(), wu.cpu(), "relu")[0].float()
+        else:
+            dg, du, wg, wu = new(T, K), new(T, K), whole(rng, K, N).bfloat16().cuda(), whole(rng, K, N).bfloat16().cuda()
+            dg[last], du[last] = (whole(rng, 3, K).bfloat16().cuda() for _ in range(2))
+            zs.glu_input_grad(dg, du, wg, wu, out)
+            want = dg[last].cpu().double() @ wg.cpu().double() + du[last].cpu().double() @ wu.cpu().double()
+        torch.cuda.synchronize()
+        assert same(out[last], want, torch.bfloat16)
+        assert not out[: T - 3].any()
+        del out

@@ -43,3 +43,12 @@ def test_every_tile_of_the_orthogonalised_update_is_tested(choices):
     assert {side for side, _ in reached["gram"]} == {32, 64, 128, 192, 256} == {side for side, split in reached["gram"] if split}
     assert {side for side, _ in reached["poly"]} == {32, 64, 128, 192, 256}
     assert {side for side, _ in reached["apply"]} == {32, 64, 128, 192, 256}
+
+
+def test_large_products_keep_the_direct_loads(choices):
+    """However many small tiles the outputs are (800,000 tokens: 8.8e9 outputs), as long as large ones fit a grid; past that
+    the kernel that goes round."""
+    for op in ("forward", "input", "weight"):
+        for M, N, K in ((800_000, 11008, 4096), (800_000, 11008, 64), (4_000_000, 4096, 1376), (300_000, 32768, 64)):
+            assert choices.glu(op, M, N, K) in ("128", "128 near", "192", "256"), (op, M, N, K)
+        assert choices.glu(op, 2 ** 31 - 1, 2 ** 31 - 1, 64) == "any"
