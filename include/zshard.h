@@ -643,7 +643,10 @@ typedef struct zs_muon_hp {
 } zs_muon_hp;
 
 /* Bytes of workspace for these sizes (0 for an empty batch, and for sizes past
-   the limits).  About 8 bytes a value and 8 a value of the smaller square. */
+   the limits).  About 8 bytes a value and 8 a value of the smaller square (4 where
+   the shorter side is at most 64), with sides padded to multiples of 32, 4 bytes
+   for each 1000 values, and up to 70 MB for split sums.  Matrices with both sides
+   at most 128 are not padded, and nothing of their workspace is touched. */
 ZS_API size_t zs_orthogonalize_workspace_bytes(int64_t rows, int64_t cols, int64_t batch);
 
 /* out = the Newton-Schulz steps of x, for each matrix of a batch.  x in x_format,

@@ -78,7 +78,7 @@ __global__ __launch_bounds__(256) void ns_mean(const MeanArgs a) {
     }
   }
   sum = block_sum(sum, lds);
-  if (threadIdx.x == 0) a.partials[(int64_t)blockIdx.y * kMostPartials + blockIdx.x] = sum;
+  if (threadIdx.x == 0) a.partials[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = sum;
 }
 
 // The squares of given matrices, summed the same way.
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(256) void ns_norm(const NormArgs a) {
     for (int k = 0; k < 8; ++k) sum += (double)v[k] * (double)v[k];
   }
   sum = block_sum(sum, lds);
-  if (threadIdx.x == 0) a.partials[(int64_t)blockIdx.y * kMostPartials + blockIdx.x] = sum;
+  if (threadIdx.x == 0) a.partials[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = sum;
 }
 
 // ---------------------------------------------------------------------------
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(256) void ns_pack(const PackArgs a) {
     for (int i = tid; i < a.n_counters; i += 256) a.counters[(int64_t)blockIdx.y * a.n_counters + i] = 0;
   }
   double sum = 0.0;
-  for (int i = tid; i < a.n_partials; i += 256) sum += a.partials[(int64_t)blockIdx.y * kMostPartials + i];
+  for (int i = tid; i < a.n_partials; i += 256) sum += a.partials[(int64_t)blockIdx.y * a.n_partials + i];
   sum = block_sum(sum, sums);
   const double per = sum == 0.0 ? 0.0 : (double)kUnit / __builtin_sqrt(sum);
   const int64_t r0 = (int64_t)(blockIdx.x / a.tiles_n) * 64, c0 = (int64_t)(blockIdx.x % a.tiles_n) * 64;  // in X0
@@ -507,7 +507,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ns_tile(const NsGemm a, uint32
 struct NsLayout {
   int64_t m, n;          // short and long side, padded
   Choice gram, poly, apply;
-  int64_t n_counters;
+  int64_t n_partials, n_counters;  // of a matrix
   size_t at_partials, at_counters, at_x[2], at_s, at_b, at_sums, bytes;
 };
 size_t sums_bytes(const Choice& c, int64_t batch) {
@@ -518,9 +518,12 @@ NsLayout layout_of(int64_t rows, int64_t cols, int64_t batch) {
   NsLayout l{};
   l.m = padded(rows < cols ? rows : cols);
   l.n = padded(rows < cols ? cols : rows);
+  const bool slab = l.m <= kSlabSide;  // no polynomial in memory, no product after it
   l.gram = choose(l.m, l.m, l.n, batch, true);
-  l.poly = choose(l.m, l.m, l.m, batch, true);
-  l.apply = choose(l.m, l.n, l.m, batch, false);
+  l.poly = slab ? Choice{} : choose(l.m, l.m, l.m, batch, true);
+  l.apply = slab ? Choice{} : choose(l.m, l.n, l.m, batch, false);
+  const int64_t want = (rows * cols + 8 * 256 - 1) / (8 * 256);
+  l.n_partials = want < kMostPartials ? want : kMostPartials;
   l.n_counters = 1;
   size_t sums = 0;
   for (const Choice& c : {l.gram, l.poly, l.apply}) {
@@ -533,11 +536,11 @@ NsLayout layout_of(int64_t rows, int64_t cols, int64_t batch) {
     at += (bytes + 255) / 256 * 256;
     return here;
   };
-  l.at_partials = take((size_t)batch * kMostPartials * 8);
+  l.at_partials = take((size_t)batch * (size_t)l.n_partials * 8);
   l.at_counters = take((size_t)batch * (size_t)l.n_counters * 4);
   for (int i = 0; i < 2; ++i) l.at_x[i] = take((size_t)batch * (size_t)l.m * (size_t)l.n * 4);
   l.at_s = take((size_t)batch * (size_t)l.m * (size_t)l.m * 4);
-  l.at_b = take((size_t)batch * (size_t)l.m * (size_t)l.m * 4);
+  l.at_b = take(slab ? 0 : (size_t)batch * (size_t)l.m * (size_t)l.m * 4);
   l.at_sums = take(sums);
   l.bytes = at;
   return l;
@@ -564,16 +567,21 @@ hipError_t gemm_launch(const NsGemm& given, const Choice& c, int64_t batch, hipS
 }  // namespace
 
 size_t ns_workspace_bytes(int64_t rows, int64_t cols, int64_t batch) {
+  if (one_workgroup(rows, cols)) {
+    // not touched: asked for as for the others, X twice, S and the polynomial, so that what a call accepts does not hang on
+    // where a matrix is kept
+    const int64_t side = rows < cols ? rows : cols;
+    return (size_t)(batch * 8 * side * (rows + cols)) + 256;
+  }
   return layout_of(rows, cols, batch).bytes + 256;  // and the way to a 256-byte boundary
 }
 
 hipError_t launch_ns(const NsProblem& p, void* workspace, hipStream_t stream) {
-  if (p.rows <= kSmallSide && p.cols <= kSmallSide) return launch_ns_small(p, stream);
+  if (one_workgroup(p.rows, p.cols)) return launch_ns_small(p, stream);
   const NsLayout l = layout_of(p.rows, p.cols, p.batch);
   char* const ws = (char*)(((uintptr_t)workspace + 255) / 256 * 256);
   const int64_t n = p.rows * p.cols;
-  const int64_t want = (n + 8 * 256 - 1) / (8 * 256);
-  const int32_t parts = (int32_t)(want < kMostPartials ? want : kMostPartials);
+  const int32_t parts = (int32_t)l.n_partials;
   double* const partials = (double*)(ws + l.at_partials);
   const dim3 first_grid((unsigned)parts, (unsigned)p.batch);
   PackArgs k{};

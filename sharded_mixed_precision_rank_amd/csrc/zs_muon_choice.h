@@ -9,6 +9,7 @@ namespace zs {
 namespace ns {
 
 constexpr int64_t kSmallSide = 128;  // matrices with both sides up to this are done by a workgroup each
+inline bool one_workgroup(int64_t rows, int64_t cols) { return rows <= kSmallSide && cols <= kSmallSide; }
 constexpr int64_t kSlabSide = 64;    // with the shorter up to this, by two kernels a step: S, and the rest
 
 inline int64_t padded(int64_t n) { return (n + 31) / 32 * 32; }

@@ -403,3 +403,20 @@ def test_a_layers_training_steps(zs):
         most = 3 * (hp["lr"] * hp["scale"] * ref.bound(5, N, K) * (2 * min(N, K)) ** 0.5 + 2.0 ** -22 * m64.norm().item())
         assert off_by <= most
         assert torch.equal(param, master.bfloat16())
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(5, 40, 700), (3, 9000, 20), (7, 129, 8), (6, 90, 140), (2, 300, 1100)])
+def test_stacks_in_workspaces_of_the_exact_size(zs, batch, rows, cols):
+    """Every matrix of a stack within the bound, and the same bits beside one of NaN; nothing outside the workspace is written."""
+    x = gradients(batch, batch, rows, cols)
+    ws = Guarded(zs, rows, cols, batch)
+    out, again = torch.empty_like(x), torch.empty_like(x)
+    zs.orthogonalize(x, out, ws.t)
+    for i in range(batch):
+        assert off(out[i], ref.steps_of(x[i])) <= ref.bound(5, rows, cols)
+    x[1] = math.nan
+    zs.orthogonalize(x, again, ws.t)
+    torch.cuda.synchronize()
+    keep = [i for i in range(batch) if i != 1]
+    assert torch.equal(again[keep], out[keep]) and torch.isnan(again[1]).all()
+    assert ws.untouched_outside()

@@ -119,3 +119,15 @@ def test_binding_refuses():
 def test_reduce_muon_refuses_what_leaves_fp32_when_folded(hp):
     """lr * scale and 1 - lr * weight_decay are fp32 values of the step: past that range, inf * 0 would be NaN in the master."""
     assert zs.STATUS[muon(**hp)] == R and b"fp32" in LIB.zs_last_error(), LIB.zs_last_error()
+
+
+def test_workspace_of_stacks_is_what_they_need():
+    """No room for sums that are not made, for padding of matrices that a workgroup keeps to itself, or for a polynomial that
+    lies nowhere."""
+    many = 65535
+    for rows, cols in ((8, 8), (1, 128), (100, 30), (128, 128)):
+        assert zs.orthogonalize_workspace_bytes(rows, cols, many) <= many * 8 * min(rows, cols) * (rows + cols) + 256
+    # 32 x 160 padded: X twice and S; a partial sum and a counter
+    assert zs.orthogonalize_workspace_bytes(129, 8, many) <= many * (8 * 32 * 160 + 4 * 32 * 32 + 16) + 2048
+    # 96 x 160: the polynomial too; 9 partial sums, at most 6 counters
+    assert zs.orthogonalize_workspace_bytes(90, 140, many) <= many * (8 * 96 * (160 + 96) + 9 * 8 + 6 * 4) + 2048
