@@ -124,6 +124,9 @@ __device__ __forceinline__ i32x4 inside(int left) {
 // operands staged through registers 16 bytes at a time, 64 of the summed axis a
 // stage, four stages ahead of the matrix instructions; two buffers in LDS and
 // one barrier a stage.  Forward: 32 columns of gate beside the same 32 of up.
+// (Addresses and bounds of four stages are more scalar values than there are
+// registers: 64 of them forward, 106 in the input gradient lie in lanes of vector
+// registers, none in memory.)
 // ---------------------------------------------------------------------------
 constexpr int kAnyTile = 64;
 
