@@ -83,24 +83,15 @@ __device__ __forceinline__ void store_grad(const GluGemm& a, int p, int64_t i, i
 template <int FMT, int RUN, bool PAST>
 __device__ __forceinline__ void store_gated(const GluGemm& a, int64_t m, int64_t n, const float* gate, const float* up) {
   if (m >= a.M || n >= a.N) return;
-  float h[RUN], none;
+  float h[RUN], none[RUN];
   switch (a.act) {
-    case ZS_ACT_SILU:
-#pragma unroll
-      for (int r = 0; r < RUN; ++r) h[r] = act_of<ZS_ACT_SILU, false>(gate[r], none) * up[r];
-      break;
-    case ZS_ACT_GELU:
-#pragma unroll
-      for (int r = 0; r < RUN; ++r) h[r] = act_of<ZS_ACT_GELU, false>(gate[r], none) * up[r];
-      break;
-    case ZS_ACT_GELU_TANH:
-#pragma unroll
-      for (int r = 0; r < RUN; ++r) h[r] = act_of<ZS_ACT_GELU_TANH, false>(gate[r], none) * up[r];
-      break;
-    default:
-#pragma unroll
-      for (int r = 0; r < RUN; ++r) h[r] = act_of<ZS_ACT_RELU, false>(gate[r], none) * up[r];
+    case ZS_ACT_SILU: acts_of<ZS_ACT_SILU, false, RUN>(gate, h, none); break;
+    case ZS_ACT_GELU: acts_of<ZS_ACT_GELU, false, RUN>(gate, h, none); break;
+    case ZS_ACT_GELU_TANH: acts_of<ZS_ACT_GELU_TANH, false, RUN>(gate, h, none); break;
+    default: acts_of<ZS_ACT_RELU, false, RUN>(gate, h, none);
   }
+#pragma unroll
+  for (int r = 0; r < RUN; ++r) h[r] = h[r] * up[r];
   store_run_as<FMT, RUN, PAST>(a.out[0], nullptr, m * a.ldo[0] + n, a.N - n, h);
   if (a.out[1] != nullptr) {
     store_run_as<FMT, RUN, PAST>(a.out[1], nullptr, m * a.ldo[1] + n, a.N - n, gate);

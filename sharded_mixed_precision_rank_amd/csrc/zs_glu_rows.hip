@@ -17,13 +17,13 @@ using namespace dev;
 template <int FMT, int ACT>
 __device__ __forceinline__ void gate_grads(const float (&dh)[8], const float (&gate)[8], const float (&up)[8], float (&dg)[8],
                                            float (&du)[8], float (&h)[8]) {
+  float value[8], slope[8];
+  acts_of<ACT, true, 8>(gate, value, slope);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    float slope;
-    const float v = act_of<ACT, true>(gate[k], slope);
-    dg[k] = dh[k] * up[k] * slope;
-    du[k] = dh[k] * v;
-    h[k] = v * up[k];
+    dg[k] = dh[k] * up[k] * slope[k];
+    du[k] = dh[k] * value[k];
+    h[k] = value[k] * up[k];
   }
 }
 
