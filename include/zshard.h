@@ -570,7 +570,9 @@ ZS_API zs_status zs_glu_forward(const void* x, int64_t ld_x, const void* w_gate,
 
 /* dgate = dh * up * act'(gate), dup = dh * act(gate).  h: NULL, or where
    act(gate) * up is written again, so that it need not be kept for the gradient
-   of the projection behind it.  dgate may be gate itself, dup up itself and h dh
+   of the projection behind it: of gate and up as they are given, rounded to 16
+   bits, while zs_glu_forward's h is made of the unrounded sums, so the two differ
+   by those roundings.  dgate may be gate itself, dup up itself and h dh
    itself (the same address and ld).  Errors as zs_glu_forward. */
 ZS_API zs_status zs_glu_backward(const void* dh, int64_t ld_dh, const void* gate, const void* up, int64_t ld_gu,
                                  int32_t format, int64_t T, int64_t N, int32_t act, void* dgate, void* dup, int64_t ld_d,

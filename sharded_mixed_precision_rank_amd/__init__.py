@@ -1016,8 +1016,8 @@ def glu_forward(x, w_gate, w_up, h, gate=None, up=None, act="silu", stream=None)
 
 def glu_backward(dh, gate, up, dgate, dup, h=None, act="silu", stream=None) -> None:
     """``dgate`` = dh * up * act'(gate) and ``dup`` = dh * act(gate) (all T x N, bf16 or fp16), from what
-    :func:`glu_forward` kept.  ``h``: where act(gate) * up is written again.  ``dgate`` may be ``gate`` itself, ``dup``
-    ``up`` and ``h`` ``dh``; see zs_glu_backward."""
+    :func:`glu_forward` kept.  ``h``: where act(gate) * up is written again, of the rounded gate and up (the forward pass's is of
+    the unrounded sums).  ``dgate`` may be ``gate`` itself, ``dup`` ``up`` and ``h`` ``dh``; see zs_glu_backward."""
     dp, T, N, dld, fmt = _matrix(dh, _Q8_DY, "dh")
     gp, upp, gld = _pair(gate, up, ("gate", "up"), dh, (T, N))
     dgp, dupp, ddld = _pair(dgate, dup, ("dgate", "dup"), dh, (T, N))
