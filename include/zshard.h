@@ -617,8 +617,11 @@ ZS_API zs_status zs_glu_weight_grad(const void* dgate, const void* dup, int64_t 
  * (rows <= cols; a matrix with more rows goes by its transpose, which is the
  * same polynomial of its singular values).  The norm is summed in double; the
  * products' operands are held in 22 bits (two fp16 parts), their sums in fp32:
- * results are about as near to exact ones as plain fp32 products would be (1e-6
- * of |X| for five default steps; the steps magnify roundings of directions with
+ * results are about as near to exact ones as plain fp32 products would be.  Five
+ * default steps, measured, relative to the result's 2-norm: 1.1e-6 at 128 x 128,
+ * 2.4e-6 at 1001 x 517, 3.2e-6 at 4096 x 4096, 4.5e-6 at 11008 x 4096 (fp32
+ * products: 1.4e-6, 3.0e-6, 4.8e-6, 8.0e-6), and 2.0e-5 (2.3e-5) for matrices of
+ * a sixteenth of full rank (the steps magnify roundings of directions with
  * small singular values, by up to a each).  A matrix of zeros gives zeros; one
  * with a NaN or an infinity gives NaN throughout, and nothing else in its batch
  * changes.  Coefficients that take entries of X, S or b S + c S^2 past 15.9 end

@@ -6,8 +6,8 @@
 // the smaller of the two squares.  The polynomial lifts small singular values by
 // a = 3.4 each step, and a rounding of X with them: with X, S and b S + c S^2
 // kept in one fp16 (11 bits) results were 0.1-1% off, in bf16 1-9%.  They are
-// kept as two fp16 parts, hi + lo (22 bits), which leaves about 1e-6, as far as
-// fp32 products are off.  A product is then three of the parts, hi hi + hi lo +
+// kept as two fp16 parts, hi + lo (22 bits), which leaves 1e-6 (128 x 128) to 4.5e-6
+// (11008 x 4096), where fp32 products are 1.4e-6 to 8e-6 off.  A product is then three of the parts, hi hi + hi lo +
 // lo hi (lo lo is below the last bit), at the fp16 rate with fp32 sums.
 //
 // Values are held times 2^12: the largest entry of X, S and b S + c S^2 is about

@@ -54,3 +54,13 @@ def test_default_steps_in_large_tiles(zs, batch, rows, cols):
 def test_the_update_in_large_tiles(zs, shape, nesterov):
     """Master and working copy from the last product's tiles of 192 and 256, turned and not, bit for bit."""
     muon.test_reduce_muon(zs, shape, 2, nesterov)
+
+
+@pytest.mark.parametrize("rows,cols,stated", [(128, 128, 1.1e-6), (1001, 517, 2.4e-6), (4096, 4096, 3.2e-6), (11008, 4096, 4.5e-6)])
+def test_five_default_steps_are_as_near_as_the_header_says(zs, rows, cols, stated):
+    """Relative to the result's norm; a tenth more for other values than the header's."""
+    x = muon.gradients(rows + cols, rows, cols)
+    out = torch.empty_like(x)
+    zs.orthogonalize(x, out)
+    want = ref.steps_of(x)
+    assert ((out.double() - want).norm() / want.norm()).item() <= 1.1 * stated
