@@ -22,11 +22,16 @@ constexpr int64_t kMostTiles = 1 << 22;  // workgroups along a grid's first axis
 
 // The kernel of a product with rows on 4-byte boundaries, by the time it takes: a start, and so much a stage of 64 of the summed axis,
 // between `few` for a few workgroups and `full` for as many as run at once; more go in rounds (half overlapped) with a
-// start of their own.  us, fitted to 54 shapes from 1 to 9683 tokens on 256 compute units, inputs from memory: off by 6 to
-// 20%, and what it picks is 1.0 to 1.8% behind the best kernel's time in the mean.  For example, forward: 1 x 1024 x 1024 4.9 by
-// kFew, 6.4 by k64x32, 7.8 by k64; 61 x 4096 x 4096 55 / 18.1 / 20.7, 27.2 by k128; 333 x 11008 x 4096 136 by k64, 96 by k128, 88 by k192,
-// 100 by k256; input gradient: 61 x 4096 x 4096 23.9 by kSplit, 37 by k32, 67 by k128; 1025 x 1376 x 4096 118 by kSplit, 56 by k128, 43 by
-// k128Near, 60 by k256; weight gradients: 61 x 4096 x 4096 25.7 by k64, 22.9 by k128Near, 20.4 by k256.
+// start of their own.  us of the kernels, fitted to 54 shapes from 1 to 9683 tokens on 256 compute units, inputs from
+// memory and outputs in 16 bits: off by 6 to 20% there.  Of calls among others they are 0.4 to 1.25 times what those take, 0.89
+// forward, 0.91 input gradient and 0.78 weight gradients in the median of 88 products with sizes drawn from 1 to 16384
+// tokens and 256 to 11008 features (a call's own 4 us, fp32 outputs and what is added to them are not in them).  What
+// counts is the order that they put the kernels in: there the pick was 1.7, 0.8 and 1.4% behind the best kernel in
+// the mean, 16, 8 and 8% at worst.  For example (predicted), forward: 1 x 11008 x 4096 39.9 by k64 (28.5), 39.6 by k128 (33.5), 41.3 by kFew
+// (38.8); 333 x 11008 x 4096 85.8 by k192 (69.2), 97.1 by k128 (92.7), 97.0 by k256 (92.7); 1000 x 1371 x 1000, kept, 17.0 by k128
+// (11.8), 19.8 by k64 (16.6); input gradient: 61 x 4096 x 4096 27.9 by kSplit (24.1), 35.7 by k32 (37.9); weight gradients: 61 x 4096 x
+// 4096 22.4 by k128Near (22.4), 19.6 by k256 (22.6); 1025 x 1376 x 4096 in bf16 30.6 by k256 (32.4), 33.3 by k128Near (37.5), in fp32
+// 33.9 and 36.5, added to fp32 sums 50.8 and 53.9.
 enum class GluTile : int32_t { kAny, kThrough, kFew, kSplit, k64x32, k32, k64, k64x128, k128, k128Near, k192, k256 };
 struct TileCost {
   GluTile tile;

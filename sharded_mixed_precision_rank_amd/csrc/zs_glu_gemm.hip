@@ -283,13 +283,15 @@ hipError_t any_launch(const GluGemm& a, hipStream_t stream) {
 // LDS reads, memory loads and matrix instructions run side by side.  One barrier
 // a stage: between its halves every wave has read all of the stage and its part
 // of the next one has landed.  THROUGH: rows at any address, which the direct loads
-// do not take, through registers (8192 x 11008 x 4096, rows one element off: 2180-2320 us).
+// do not take, through registers (8192 x 11008 x 4096, rows one element off: 2054-2312 us).
 //
 // Bound, where there are many tiles, by the matrix instructions and the clock that they
-// leave: 8192 x 11008 x 4096 in bf16, 256 x 256 tiles, 1155-1257 us forward (1180-1280
-// TFLOP/s), 1110-1172 input gradient, 1122-1143 weight gradients, matrix pipes 66-74% busy at
-// 1.5-1.65 GHz; 32 x 32 x 16 instructions on the same fragments took 1221-1344 / 1169-1184 /
-// 1169.  With few tiles by what a compute unit takes in: 333 x 11008 x 4096 85 us in 192 x 128.
+// leave: 8192 x 11008 x 4096 in bf16, 256 x 256 tiles, 1103-1249 us forward (1180-1340
+// TFLOP/s), 1192-1300 with gate and up kept, 1099-1173 input gradient, 1132-1257 weight
+// gradients, matrix pipes 65-74% busy at 1.48-1.67 GHz; 32 x 32 x 16 instructions on the same
+// fragments, in one process with these, took 1221-1344 / 1169-1184 / 1169 where these
+// took 1155-1257 / 1110-1172 / 1122-1143.  With few tiles by what a compute unit takes
+// in: 333 x 11008 x 4096 86 us in 192 x 128.
 //
 // An operand whose rows run along the summed axis lies in rows of 128 bytes,
 // read 16 bytes a lane; one whose rows lie across it (both weights in kInput,
@@ -619,7 +621,7 @@ hipError_t tile_launch(const GluGemm& a, hipStream_t stream) {
 // order: a stage of the tiled kernels takes at least 0.2 us, whatever its size,
 // for its barrier and two rounds of LDS reads.  With 32 or 64 rows a workgroup it
 // lost to the tiles (61 x 4096 x 4096: 32 and 24 us, 18 in 64 x 32).  One token, N =
-// 11008, K = 4096: 36-40 us by every kernel here, the weights' 180 MB at 4.5-5 TB/s.
+// 11008, K = 4096: 41 us, 40-44 in tiles of up to 128, the weights' 180 MB at 4.1-4.5 TB/s.
 // ---------------------------------------------------------------------------
 template <int FMT, int W>
 __global__ __launch_bounds__(W * 64, 2) void glu_few(const GluGemm a, uint32_t tiles_n) {

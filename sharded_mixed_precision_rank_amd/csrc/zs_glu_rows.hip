@@ -1,7 +1,8 @@
 // The elementwise half of the gated block's backward pass:
 //   dgate = dh * up * act'(gate),  dup = dh * act(gate),  and h = act(gate) * up again where it is asked for
 // (instead of keeping it).  Bound by memory: 10 bytes a value, 12 with h (8192 x
-// 11008 in bf16: 145 us, 6.2 TB/s, as a plain copy).  A
+// 11008 in bf16: 142-151 us, 6.1 TB/s, as a plain copy), but for gelu, by its error
+// function (among others 168-189 us, where the rest take 157-161).  A
 // thread takes 8 consecutive columns; the hardware takes vector accesses at any
 // address, so rows need no alignment, and an output may lie on the input of the
 // same place: a thread has read its 8 values before it writes them.

@@ -188,9 +188,9 @@ __global__ __launch_bounds__(256) void ns_pack(const PackArgs a) {
 // their order, so the result does not depend on who that is.
 //
 // Large products are bound by the matrix instructions and the clock under them: 4096
-// x 4096, S and the polynomial 176 us each in 192 x 192 tiles (matrix pipes busy 65% at
+// x 4096, S and the polynomial 175-178 us each in 192 x 192 tiles (matrix pipes busy 65% at
 // 1.9 GHz), B X 290 in 256 x 256 (76% at 1.8 GHz; 1420 TFLOP/s of the parts' three
-// products); S of 4096 x 11008 449, B X 830.  Small ones by a launch's start and end, 4 us, and
+// products); S of 4096 x 11008 442-458, B X 821-828.  Small ones by a launch's start and end, 4 us, and
 // what a compute unit takes in.
 // ---------------------------------------------------------------------------
 enum class NsOp : int32_t { kGram = 0, kPoly = 1, kApply = 2 };
